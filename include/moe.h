@@ -510,6 +510,163 @@ MOE_API moe_status moe_forward_w4(const moe_config *cfg, const void *x, const fl
                                   double *loss, float *logits_out, int32_t *n_dropped, void *ws, size_t ws_bytes,
                                   moe_stream_t stream);
 
+/* ---- Experts in e4m3 with one scale per block of 128 ----------------------
+ * The finest-grained form of the quantized experts ("Fine-tuning and serving
+ * MoE models", Serving: quantize the experts since memory binds) that keeps
+ * fp32 scales: every weight matrix [out, in] holds e4m3 codes with one fp32
+ * scale per 128 x 128 block, every activation row one fp32 scale per 128
+ * values.  The products of each block of 128 of K run on the tensor cores
+ * (fp32 accumulation) and are scaled and summed in fp32:
+ *   C[r][n] = sum_b xs[r][b] * ws[n / 128][b] * sum_{k in block b} x8[r][k] w8[n][k]
+ *   quantization (moe_quantize_rows_block, moe_rmsnorm, and H on the device):
+ *     per run of 128 values of a row (the last may be shorter) a = max(max |v|,
+ *     2^-100), scale = a / 448, code = e4m3(v * (448 / a)), round to nearest
+ *     even.  H is quantized from its fp32 values (no bf16 rounding before).  A
+ *     NaN gives a NaN code; an infinity makes its block's scale infinite.
+ *   weights: codes in the nn.Linear [out, in] layout stacked over experts;
+ *     scales [.., ceil(out / 128), sld bytes], the first ceil(in / 128) floats
+ *     of a row used.
+ *   activations: scale rows of sld bytes, the first ceil(width / 128) floats
+ *     used.
+ * sld: a multiple of 16, at least 4 * ceil(K / 128) for K = d_model, d_ff and
+ * d_ff_shared.  Only bf16 layers with d_model, d_ff and d_ff_shared multiples
+ * of 16 (else MOE_ERR_UNSUPPORTED); a last block may be shorter than 128.  All
+ * pointers in the struct are device pointers, 16-byte aligned; the struct is
+ * read during the call.  Forward only.                                       */
+typedef struct {
+    const uint8_t *W1;    const float *W1_scale;    /* [E, d_ff, d_model], [E, ceil(d_ff/128), sld]    */
+    const uint8_t *Wu;    const float *Wu_scale;    /* SwiGLU W_up (same shapes), else NULL            */
+    const uint8_t *W2;    const float *W2_scale;    /* [E, d_model, d_ff], [E, ceil(d_model/128), sld] */
+    const uint8_t *Wsh_g; const float *Wsh_g_scale; /* shared expert, same layouts, or NULL            */
+    const uint8_t *Wsh_u; const float *Wsh_u_scale;
+    const uint8_t *Wsh_d; const float *Wsh_d_scale;
+    int32_t sld;                                    /* scale row stride in bytes                       */
+} moe_fp8_block_experts;
+
+/* 1 x 128 quantization of a bf16 matrix: `rows` rows of `cols` values (row
+ * stride ld_in elements) -> codes [rows, ld_out bytes] and scale rows ld_scale
+ * bytes apart.  cols, ld_in and ld_out multiples of 8, ld_scale a multiple of
+ * 4 and at least 4 * ceil(cols / 128); `in` 16-byte, codes 8-byte aligned.
+ * Bytes behind a row's codes and scales are left untouched.                  */
+MOE_API moe_status moe_quantize_rows_block(const void *in, int64_t rows, int32_t cols, int64_t ld_in, uint8_t *codes,
+                                           int64_t ld_out, float *scale, int64_t ld_scale, moe_stream_t stream);
+
+/* moe_grouped_ffn with block-scaled e4m3 experts: x8_perm [T*top_k, d_model]
+ * codes of the packed rows with their scale rows xs_perm (w->sld bytes apart);
+ * x8 / xs the codes and scale rows of x [T, d_model] (the shared expert's
+ * input; NULL without one); b1, b2 fp32 as in moe_grouped_ffn.  Output y_perm
+ * as in moe_grouped_ffn (bf16; routed rows past offsets[E] untouched).  H's
+ * codes and scales live in ws.  offsets that are no prefix sums within
+ * T*top_k rows are recorded as MOE_ERR_DEVICE_BOUNDS and the group is skipped. */
+MOE_API moe_status moe_grouped_ffn_fp8_block(const moe_config *cfg, const uint8_t *x8_perm, const float *xs_perm,
+                                             const int32_t *offsets, const float *row_gate,
+                                             const moe_fp8_block_experts *w, const float *b1, const float *b2,
+                                             const uint8_t *x8, const float *xs, void *y_perm, void *ws,
+                                             size_t ws_bytes, moe_stream_t stream);
+
+/* ---- Group-limited routing -------------------------------------------------
+ * The E experts form n_group equal groups of consecutive ids (the experts of
+ * one node), and a token only uses experts of its topk_group best groups,
+ * which bounds the ranks its row travels to ("Fine-Tuning Mixture of Experts
+ * (MoE) Models: Router Optimization Techniques", Why It Matters 2: dispatch
+ * traffic).  With the scores and selection keys of moe_router_topk:
+ *   group score = the sum of the group's group_top (1 or 2) largest keys;
+ *   the topk_group groups of the largest score stay, the top_k largest keys
+ *   inside them are chosen, best first; equal keys and equal groups go to the
+ *   lower id; gates as in moe_router_topk, times gate_scale.
+ * Keys are compared by their 64-bit values.  A logit of -inf is an expert that
+ * is chosen last; a row whose chosen scores sum to 0 gets gates of 0; NaN keys
+ * rank below all others.  n_group divides E, group_top <= E / n_group, top_k <=
+ * topk_group * E / n_group, gate_scale > 0 (else MOE_ERR_INVALID_ARG).
+ * n_group = 1 is the unrestricted choice.  The struct is a host object read
+ * during the call.                                                           */
+typedef struct {
+    int32_t n_group;
+    int32_t topk_group;
+    int32_t group_top;
+    float gate_scale;
+} moe_route_groups;
+
+/* The selection alone, from logits [T, E] fp32 (T, E, top_k, score and renorm
+ * of cfg are used): idx [T, top_k], gate [T, top_k], and, unless psum is NULL,
+ * the score sums [moe_router_blocks(cfg), E] that moe_balance_stats takes.   */
+MOE_API moe_status moe_route_select(const moe_config *cfg, const moe_route_groups *groups, const float *logits,
+                                    const float *sel_bias, int32_t *idx, float *gate, float *psum,
+                                    moe_stream_t stream);
+/* Its gradient: dlogits [T, E] of  sum dgate * gate + alpha * L_aux  (L_aux =
+ * E sum_e f_e P_e), for the chosen idx [T, top_k]; counts [E] (the f_e of the
+ * balance loss; NULL with alpha = 0).  The choice and f_e carry no gradient; an
+ * id outside [0, E) contributes none.                                        */
+MOE_API moe_status moe_route_backward(const moe_config *cfg, const moe_route_groups *groups, const float *logits,
+                                      const int32_t *idx, const float *dgate, const int32_t *counts, float alpha,
+                                      float *dlogits, moe_stream_t stream);
+/* moe_router_topk, moe_forward, moe_forward_train and moe_backward with
+ * group-limited routing: the same arguments after `groups`.  A backward pass
+ * takes the groups of its forward pass.                                      */
+MOE_API moe_status moe_router_topk_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x,
+                                          const float *Wr, const float *logit_bias, const float *sel_bias,
+                                          int32_t *idx, float *gate, float *logits_out, float *psum, void *ws,
+                                          size_t ws_bytes, moe_stream_t stream);
+MOE_API moe_status moe_forward_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr,
+                                      const float *logit_bias, const float *sel_bias, const void *W1, const float *b1,
+                                      const void *Wu, const void *W2, const float *b2, const void *Wsh_g,
+                                      const void *Wsh_u, const void *Wsh_d, void *y, int32_t *idx, float *gate,
+                                      int32_t *counts, float *f, float *P, double *loss, float *logits_out,
+                                      int32_t *n_dropped, void *ws, size_t ws_bytes, moe_stream_t stream);
+MOE_API moe_status moe_forward_train_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr,
+                                      const float *logit_bias, const float *sel_bias, const void *W1, const float *b1,
+                                      const void *Wu, const void *W2, const float *b2, const void *Wsh_g,
+                                      const void *Wsh_u, const void *Wsh_d, void *y, int32_t *idx, float *gate,
+                                      int32_t *counts, float *f, float *P, double *loss, float *logits_out,
+                                      int32_t *n_dropped, void *ws, size_t ws_bytes,
+                                      void *bwd_ws, size_t bwd_ws_bytes, moe_stream_t stream);
+MOE_API moe_status moe_backward_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x,
+                                       const float *Wr, const void *W1, const float *b1, const void *Wu,
+                                       const void *W2, const float *b2, const void *Wsh_g, const void *Wsh_u,
+                                       const void *Wsh_d, const int32_t *idx, const float *gate, const float *logits,
+                                       const int32_t *counts, const void *dy, float alpha, void *dx, float *dWr,
+                                       float *dlogit_bias, float *dW1, float *db1, float *dWu, float *dW2,
+                                       float *db2, float *dWsh_g, float *dWsh_u, float *dWsh_d, void *fwd_ws,
+                                       size_t fwd_ws_bytes, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_forward with block-scaled e4m3 experts: router on the bf16 x (groups
+ * NULL: moe_router_topk's selection), x's codes and scale rows permuted with
+ * the rows, the grouped FFN above, combine, statistics.  x8 [T, d_model] and xs
+ * (scale rows w->sld bytes apart) are x's codes and scales, as moe_rmsnorm
+ * writes them beside x; both NULL: x is quantized here.                      */
+MOE_API moe_status moe_forward_fp8_block(const moe_config *cfg, const moe_route_groups *groups, const void *x,
+                                         const uint8_t *x8, const float *xs, const float *Wr, const float *logit_bias,
+                                         const float *sel_bias, const moe_fp8_block_experts *w, const float *b1,
+                                         const float *b2, void *y, int32_t *idx, float *gate, int32_t *counts,
+                                         float *f, float *P, double *loss, float *logits_out, int32_t *n_dropped,
+                                         void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---- RMS norm with the residual's addition and an 8-bit output ---------------
+ * What a transformer block runs before the layer: for each of `rows` rows of d
+ * values of dtype (moe_dtype)
+ *   z = x + residual (x alone when NULL), h = z rounded to dtype,
+ *   v = z / sqrt(mean(z^2) + eps) * weight, y = v rounded to dtype,
+ *   codes / scale: the 1 x 128 quantization of v (moe_fp8_block_experts above),
+ *   scale rows ld_scale bytes apart.
+ * Everything before a rounding is fp32: v comes from the unrounded z, the codes
+ * from the unrounded v.  h, y, and codes with scale may each be NULL (not
+ * all).  h may be residual or x itself, y may be x itself; other overlaps are
+ * not allowed.  weight [d] fp32.  d a multiple of 8, at most 32768 (else
+ * MOE_ERR_UNSUPPORTED).  Pointers 16-byte aligned (codes 8, scale 4).        */
+MOE_API moe_status moe_rmsnorm(int32_t dtype, int64_t rows, int32_t d, const void *x, const void *residual,
+                               const float *weight, float eps, void *h, void *y, uint8_t *codes, float *scale,
+                               int64_t ld_scale, moe_stream_t stream);
+/* Its backward pass at the stored h: dy the gradient of y, dres (may be NULL)
+ * the gradient that reaches h from the residual stream.  dh = dres + the norm's
+ * gradient (the gradient of x and of residual alike), rounded once to dtype; it
+ * may be dy or dres itself.  dweight [d] fp32, summed in a fixed order.  ws:
+ * moe_rmsnorm_backward_workspace_size(rows, d) bytes of scratch, 256-byte
+ * aligned (0 on a bad argument).                                             */
+MOE_API size_t moe_rmsnorm_backward_workspace_size(int64_t rows, int32_t d);
+MOE_API moe_status moe_rmsnorm_backward(int32_t dtype, int64_t rows, int32_t d, const void *h, const float *weight,
+                                        float eps, const void *dy, const void *dres, void *dh, float *dweight,
+                                        void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Auxiliary-loss-free bias update, to run after a training step on the
  * counts that step's routing produced ("Fine-Tuning Mixture of Experts (MoE)
  * Models: Router Optimization Techniques", How It Works 2, and its router

@@ -106,7 +106,8 @@ size_t moe_backward_workspace_size(const moe_config *cfg) {
     return bwd_layout(cfg).total;
 }
 
-moe_status moe_backward(const moe_config *cfg, const void *x, const float *Wr, const void *W1, const float *b1,
+// gate_scale: the factor of every gate (1, or the routing groups').
+static moe_status backward_impl(const moe_config *cfg, float gate_scale, const void *x, const float *Wr, const void *W1, const float *b1,
                         const void *Wu, const void *W2, const float *b2, const void *Wsh_g, const void *Wsh_u,
                         const void *Wsh_d, const int32_t *idx, const float *gate, const float *logits,
                         const int32_t *counts, const void *dy, float alpha, void *dx, float *dWr, float *dlogit_bias,
@@ -193,6 +194,7 @@ moe_status moe_backward(const moe_config *cfg, const void *x, const float *Wr, c
     aux.dZ = dZ; aux.dh = dh; aux.dh_bf16 = dh16; aux.dh_ld = E64;
     aux.dX_rows = dXr; aux.dX_shared = shared ? dXs : nullptr; aux.dX_router = dXrt; aux.dx = dx;
     aux.alpha = alpha;
+    aux.gate_scale = gate_scale;
     aux.T = T; aux.d = d; aux.E = E; aux.k = k; aux.score = cfg->score; aux.renorm = cfg->renorm; aux.num_sms = nsm;
 
     // ---- 1. dZ = gate * dy[token] for every packed row
@@ -313,6 +315,32 @@ moe_status moe_backward(const moe_config *cfg, const void *x, const float *Wr, c
             return cuda(e, "dbeta");
     }
     return MOE_OK;
+}
+
+moe_status moe_backward(const moe_config *cfg, const void *x, const float *Wr, const void *W1, const float *b1,
+                        const void *Wu, const void *W2, const float *b2, const void *Wsh_g, const void *Wsh_u,
+                        const void *Wsh_d, const int32_t *idx, const float *gate, const float *logits,
+                        const int32_t *counts, const void *dy, float alpha, void *dx, float *dWr, float *dlogit_bias,
+                        float *dW1, float *db1, float *dWu, float *dW2, float *db2, float *dWsh_g, float *dWsh_u,
+                        float *dWsh_d, void *fwd_ws, size_t fwd_ws_bytes, void *ws, size_t ws_bytes,
+                        moe_stream_t stream) {
+    return backward_impl(cfg, 1.f, x, Wr, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, idx, gate, logits, counts, dy, alpha, dx, dWr,
+                         dlogit_bias, dW1, db1, dWu, dW2, db2, dWsh_g, dWsh_u, dWsh_d, fwd_ws, fwd_ws_bytes, ws, ws_bytes,
+                         stream);
+}
+
+moe_status moe_backward_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const void *W1, const float *b1,
+                        const void *Wu, const void *W2, const float *b2, const void *Wsh_g, const void *Wsh_u,
+                        const void *Wsh_d, const int32_t *idx, const float *gate, const float *logits,
+                        const int32_t *counts, const void *dy, float alpha, void *dx, float *dWr, float *dlogit_bias,
+                        float *dW1, float *db1, float *dWu, float *dW2, float *db2, float *dWsh_g, float *dWsh_u,
+                        float *dWsh_d, void *fwd_ws, size_t fwd_ws_bytes, void *ws, size_t ws_bytes,
+                        moe_stream_t stream) {
+    moe_status s = moe::validate_groups(cfg, groups);
+    if (s != MOE_OK) return s;
+    return backward_impl(cfg, groups->gate_scale, x, Wr, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, idx, gate, logits, counts, dy, alpha, dx, dWr,
+                         dlogit_bias, dW1, db1, dWu, dW2, db2, dWsh_g, dWsh_u, dWsh_d, fwd_ws, fwd_ws_bytes, ws, ws_bytes,
+                         stream);
 }
 
 }  // extern "C"

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
         float dot = 0.f;
         for (int s = 0; s < k; ++s) {
             const int e = __shfl_sync(0xffffffffu, es, s);
-            const float dg = __shfl_sync(0xffffffffu, dgs, s);
+            const float dg = __shfl_sync(0xffffffffu, dgs, s) * a.gate_scale;
             const float pv = score_of(sc, e);
             dot += pv * dg;
 #pragma unroll
@@ -143,8 +143,9 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) dh[i] -= sc[i] * dot;
     } else if (a.score == MOE_SCORE_SOFTMAX) {
-        // renormalised over the selection: dh_sel = g (dg - <dg, g>)
-        const float dot = warp_sum(in_slot ? gs * dgs : 0.f);
+        // renormalised over the selection, times the gate factor c:
+        // dh_sel = g (dg - <dg, g> / c)
+        const float dot = warp_sum(in_slot ? gs * dgs : 0.f) / a.gate_scale;
         for (int s = 0; s < k; ++s) {
             const int e = __shfl_sync(0xffffffffu, es, s);
             const float v = __shfl_sync(0xffffffffu, gs * (dgs - dot), s);
@@ -153,13 +154,14 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
                 if (i * 32 + lane == e) dh[i] += v;
         }
     } else {
-        // sigmoid: g_s = s_{e_s} / S_sel: ds_sel = (dg - <dg, g>) / S_sel, dh = ds s (1 - s)
+        // sigmoid: g_s = c s_{e_s} / S_sel: ds_sel = (c dg - <dg, g>) / S_sel, dh = ds s (1 - s)
         const float dot = warp_sum(in_slot ? gs * dgs : 0.f);
         float ssel = 0.f;
         for (int s = 0; s < k; ++s) ssel += score_of(sc, __shfl_sync(0xffffffffu, es, s));
         for (int s = 0; s < k; ++s) {
             const int e = __shfl_sync(0xffffffffu, es, s);
-            const float v = __shfl_sync(0xffffffffu, (dgs - dot) / ssel, s);
+            // no scores left (every chosen sigmoid underflowed): gates of 0, no gradient
+            const float v = __shfl_sync(0xffffffffu, ssel == 0.f ? 0.f : (dgs * a.gate_scale - dot) / ssel, s);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 if (i * 32 + lane == e) dh[i] += v * sc[i] * (1.f - sc[i]);

@@ -273,6 +273,104 @@ cudaError_t launch_bias_update(const int32_t *counts, float *bias, double gamma,
 cudaError_t launch_routing_health(const int32_t *counts, const float *P, double *out, int T, int k, int E,
                                   cudaStream_t st);
 
+// ---- RMS norm with the residual's addition and an 8-bit output (rmsnorm.cu).
+// Arrays [rows, d] of T (bf16 or fp32), d a multiple of 8 up to 32768; the
+// scale rows of the codes are ld_scale bytes apart.
+struct RmsNormArgs {
+    const void *x, *residual;    // residual may be null
+    const float *weight;         // [d]
+    void *h, *y;                 // x + residual and its norm, each may be null
+    uint8_t *codes;              // [rows, d] e4m3, or null
+    float *scale;                // [rows, ceil(d / 128)]
+    int64_t ld_scale, rows;
+    int d;
+    float eps;
+    bool pdl;
+};
+cudaError_t launch_rmsnorm(const RmsNormArgs &a, bool bf16, cudaStream_t st);
+struct RmsNormBwdArgs {
+    const void *h, *dy, *dres;   // dres may be null
+    const float *weight;
+    void *dh;
+    float *part;                 // [rmsnorm_bwd_parts(rows), d] scratch
+    float *dweight;              // [d]
+    int64_t rows;
+    int d;
+    float eps;
+    bool pdl;
+};
+int64_t rmsnorm_bwd_parts(int64_t rows);
+cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs &a, bool bf16, cudaStream_t st);
+
+// ---- group-limited expert selection (route_groups.cu)
+struct RouteArgs {
+    const float *logits;         // [splits, T, E] partial logits, added in order
+    const float *sel_bias;       // [E] or null
+    float *logits_out;           // [T, E] the sums, or null
+    int32_t *idx;                // [T, k]
+    float *gate;                 // [T, k]
+    float *psum;                 // [ceil(T / 32), E] or null
+    int T, E, k, score, renorm, splits;
+    int n_group, topk_group, group_top;
+    float gate_scale;
+    int vec;                     // set by the launcher: rows load as whole vectors
+    bool pdl;
+};
+cudaError_t launch_route_select(const RouteArgs &a, cudaStream_t st);
+struct RouteBwdArgs {
+    const float *logits;         // [T, E]
+    const int32_t *idx;          // [T, k]
+    const float *dgate;          // [T, k]
+    const int32_t *counts;       // [E], read when alpha != 0
+    float *dlogits;              // [T, E]
+    int T, E, k, score, renorm;
+    float gate_scale, alpha;
+    int vec, vec_out;            // set by the launcher
+    bool pdl;
+};
+cudaError_t launch_route_bwd(const RouteBwdArgs &a, cudaStream_t st);
+// The router's logits and the selection from them; groups null: top-k over all
+// experts as in launch_router (router_topk.cu).
+cudaError_t launch_router_any(const RouterArgs &a, bool bf16, const moe_route_groups *groups, cudaStream_t st);
+
+// ---- experts in e4m3 with one scale per block of 128 (fp8_block.cu, fp8_block_sm100.cu)
+struct QuantBlockArgs {
+    const __nv_bfloat16 *in;
+    int64_t ld_in;
+    uint8_t *out;
+    int64_t ld_out;
+    float *scale;
+    int64_t ld_scale;            // bytes
+    int64_t rows;
+    int cols, num_sms;
+    bool pdl;
+};
+cudaError_t launch_quant_block(const QuantBlockArgs &a, cudaStream_t st);
+// dst[r] = src[row_token[r]] for r < min(*count, max_rows): rows of nb floats, ld_* bytes apart.
+cudaError_t launch_gather_scales(const float *src, int64_t ld_src, float *dst, int64_t ld_dst, int nb,
+                                 const int32_t *row_token, const int32_t *count, int64_t max_rows, int num_sms,
+                                 cudaStream_t st);
+struct FfnFp8BlockArgs {
+    const uint8_t *x_perm; const float *xs_perm;      // [routed_rows, d] codes, scale rows
+    const uint8_t *x; const float *xs;                // [T, d] (shared expert) or null
+    int64_t ld_xs, ld_xs_shared;                      // bytes between scale rows of xs_perm, of xs
+    const int32_t *offsets;                           // [E+1]
+    const float *row_gate;                            // [routed_rows]
+    const uint8_t *W1, *Wu, *W2; const float *W1s, *Wus, *W2s;
+    const uint8_t *Wsg, *Wsu, *Wsd; const float *Wsgs, *Wsus, *Wsds;
+    int64_t sld;                                      // bytes between scale rows of the weights
+    const float *b1, *b2;                             // GELU biases or null
+    uint8_t *H8; float *h_scale;                      // [routed_rows (+T), hF] codes, scale rows
+    int64_t ld_hs;                                    // bytes
+    __nv_bfloat16 *y_perm;                            // [routed_rows (+T), d]
+    int32_t *status;
+    int T, d, E, F, S, act, hF;
+    int64_t routed_rows, shared_base;
+    int num_sms;
+    bool pdl;
+};
+cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st);
+
 // ---- backward pass (bwd_sm100.cu, bwd_aux.cu)
 // One grouped GEMM C = A B^T on the tensor cores, bf16 operands, fp32
 // accumulation.  Group g owns rows offsets[g] .. offsets[g+1]: with kgroup = 0
@@ -337,6 +435,7 @@ struct BwdAuxArgs {
     const float *dX_router;      // [T, d]
     void *dx;                    // [T, d] bf16
     float alpha;
+    float gate_scale;            // factor of every gate (1 without groups)
     int T, d, E, k, score, renorm, num_sms;
 };
 cudaError_t launch_scale_rows(const BwdAuxArgs &a, int max_rows, cudaStream_t st);
@@ -361,6 +460,7 @@ cudaError_t launch_set_pair(int32_t *p, int32_t a, int32_t b, cudaStream_t st); 
 
 // Host-side helpers shared by the entry points (moe_api.cu).
 moe_status validate_config(const moe_config *cfg);        // sets the error detail
+moe_status validate_groups(const moe_config *cfg, const moe_route_groups *g);
 void set_error_detail(const char *where, const char *what);
 
 }  // namespace moe

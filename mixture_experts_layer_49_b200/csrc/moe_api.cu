@@ -42,8 +42,14 @@ struct Layout {
     // e4m3 experts (bf16 layers): codes and row scales of x, the packed rows'
     // scales (the codes themselves go to x_perm), codes and scales of H
     size_t x8, x8_scale, xperm_scale, H8, h_scale;
+    // e4m3 experts with a scale per block of 128 (codes in x8, x_perm and H8
+    // as above): scale rows of x, of the packed rows and of H
+    size_t xs, xs_perm, hs;
     size_t total;
 };
+
+// Bytes of a workspace scale row: one fp32 per 128 of `width`, whole 16 bytes.
+size_t scale_row_bytes(int width) { return ((size_t)(width + 127) / 128 * 4 + 15) / 16 * 16; }
 
 int64_t perm_rows(const moe_config *c) {
     return (int64_t)c->T * c->top_k + (c->d_ff_shared > 0 ? (int64_t)c->T : 0);
@@ -60,7 +66,7 @@ Layout layout(const moe_config *c) {
     const size_t nch = (size_t)moe::dispatch_chunks(c->T);
     size_t o = sizeof(moe::WsHeader);
     L.router_w = o;   o = align256(o + (bf16 ? moe::router_split_bytes(c->d_model, c->E) : 0));
-    L.logits = o;     o = align256(o + (bf16 ? (size_t)moe::router_logit_splits_max(c->T) * c->T * c->E * 4 : 0));
+    L.logits = o;     o = align256(o + (bf16 ? (size_t)moe::router_logit_splits_max(c->T) : 1) * c->T * c->E * 4);
     L.psum = o;       o = align256(o + nblk * c->E * 4);
     L.chunk_cnt = o;  o = align256(o + nch * c->E * 4);
     L.chunk_base = o; o = align256(o + nch * c->E * 4);
@@ -79,6 +85,9 @@ Layout layout(const moe_config *c) {
     L.xperm_scale = o; o = align256(o + f8 * Tk * 4);
     L.H8 = o;         o = align256(o + f8 * rows * hF);
     L.h_scale = o;    o = align256(o + f8 * rows * 4);
+    L.xs = o;         o = align256(o + f8 * (size_t)c->T * scale_row_bytes(c->d_model));
+    L.xs_perm = o;    o = align256(o + f8 * Tk * scale_row_bytes(c->d_model));
+    L.hs = o;         o = align256(o + f8 * rows * scale_row_bytes((int)hF));
     L.total = o;
     return L;
 }
@@ -222,6 +231,43 @@ void forget_frozen(const void *ws) {
         if (g_frozen[i].ws == ws) { g_frozen.erase(g_frozen.begin() + (long)i); return; }
 }
 
+// Experts with a scale per block of 128: as e4m3 experts, and scale rows of
+// sld bytes (a multiple of 16 that holds one fp32 per 128 of the widest K).
+moe_status check_fp8_block_cfg(const moe_config *c, int32_t sld) {
+    if (c->dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "block-scaled FP8 experts need a bf16 layer%s");
+    if (c->d_model % 16 || c->d_ff % 16 || c->d_ff_shared % 16)
+        return fail(MOE_ERR_UNSUPPORTED, "block-scaled FP8 experts need d_model, d_ff, d_ff_shared multiples of 16%s");
+    const int need = (std::max(c->d_model, std::max(c->d_ff, c->d_ff_shared)) + 127) / 128 * 4;
+    if (sld < need || sld % 16) return fail(MOE_ERR_INVALID_ARG, "sld below 4 * ceil(K / 128) or not a multiple of 16%s");
+    return MOE_OK;
+}
+
+moe_status check_fp8_block_weights(const moe_config *c, const moe_fp8_block_experts *w) {
+    NEED(w->W1); NEED(w->W1_scale); NEED(w->W2); NEED(w->W2_scale);
+    if (c->act == MOE_ACT_SWIGLU) { NEED(w->Wu); NEED(w->Wu_scale); }
+    if (c->d_ff_shared > 0) {
+        NEED(w->Wsh_g); NEED(w->Wsh_g_scale); NEED(w->Wsh_d); NEED(w->Wsh_d_scale);
+        if (c->act == MOE_ACT_SWIGLU) { NEED(w->Wsh_u); NEED(w->Wsh_u_scale); }
+    }
+    ALIGNED(w->W1, 16); ALIGNED(w->Wu, 16); ALIGNED(w->W2, 16); ALIGNED(w->Wsh_g, 16); ALIGNED(w->Wsh_u, 16);
+    ALIGNED(w->Wsh_d, 16); ALIGNED(w->W1_scale, 16); ALIGNED(w->Wu_scale, 16); ALIGNED(w->W2_scale, 16);
+    ALIGNED(w->Wsh_g_scale, 16); ALIGNED(w->Wsh_u_scale, 16); ALIGNED(w->Wsh_d_scale, 16);
+    return MOE_OK;
+}
+
+moe_status check_groups(const moe_config *c, const moe_route_groups *g) {
+    if (!g) return fail(MOE_ERR_INVALID_ARG, "NULL pointer: %s", "groups");
+    if (g->n_group < 1 || c->E % g->n_group) return fail(MOE_ERR_INVALID_ARG, "n_group does not divide E%s");
+    if (g->topk_group < 1 || g->topk_group > g->n_group) return fail(MOE_ERR_INVALID_ARG, "topk_group outside 1..n_group%s");
+    const int size = c->E / g->n_group;
+    if (g->group_top < 1 || g->group_top > 2 || g->group_top > size)
+        return fail(MOE_ERR_INVALID_ARG, "group_top must be 1 or 2 and at most E / n_group%s");
+    if (c->top_k > g->topk_group * size) return fail(MOE_ERR_INVALID_ARG, "top_k above the experts of topk_group groups%s");
+    if (!(g->gate_scale > 0.f) || !isfinite(g->gate_scale))
+        return fail(MOE_ERR_INVALID_ARG, "gate_scale must be positive and finite%s");
+    return MOE_OK;
+}
+
 moe_status check_fp8_weights(const moe_config *c, const moe_fp8_experts *w) {
     NEED(w);
     NEED(w->W1); NEED(w->W1_scale); NEED(w->W2); NEED(w->W2_scale);
@@ -348,6 +394,10 @@ moe::FfnMxArgs w4_args(const moe_config *cfg, const void *x_perm, const int32_t 
 
 namespace moe {
 moe_status validate_config(const moe_config *cfg) { return check_cfg(cfg); }
+moe_status validate_groups(const moe_config *cfg, const moe_route_groups *g) {
+    const moe_status s = check_cfg(cfg);
+    return s != MOE_OK ? s : check_groups(cfg, g);
+}
 
 namespace {
 struct SavedPreacts {
@@ -443,7 +493,8 @@ moe_status moe_router_freeze(const moe_config *cfg, const float *Wr, void *ws, s
     return MOE_OK;
 }
 
-moe_status moe_router_topk(const moe_config *cfg, const void *x, const float *Wr, const float *logit_bias,
+// groups null: top-k over all experts.
+static moe_status router_impl(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const float *logit_bias,
                            const float *sel_bias, int32_t *idx, float *gate, float *logits_out, float *psum,
                            void *ws, size_t ws_bytes, moe_stream_t stream) {
     moe_status s = check_cfg(cfg);
@@ -457,8 +508,22 @@ moe_status moe_router_topk(const moe_config *cfg, const void *x, const float *Wr
                       at<char>(ws, layout(cfg).router_w), at<float>(ws, layout(cfg).logits), status_word(ws),
                       num_sms()};
     a.split_ready = cfg->dtype == MOE_BF16 && router_split_ready(ws, Wr, cfg->d_model, cfg->E);
-    cudaError_t e = moe::launch_router(a, cfg->dtype == MOE_BF16, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = moe::launch_router_any(a, cfg->dtype == MOE_BF16, groups, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "router");
+}
+
+moe_status moe_router_topk(const moe_config *cfg, const void *x, const float *Wr, const float *logit_bias,
+                           const float *sel_bias, int32_t *idx, float *gate, float *logits_out, float *psum,
+                           void *ws, size_t ws_bytes, moe_stream_t stream) {
+    return router_impl(cfg, nullptr, x, Wr, logit_bias, sel_bias, idx, gate, logits_out, psum, ws, ws_bytes, stream);
+}
+
+moe_status moe_router_topk_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const float *logit_bias,
+                           const float *sel_bias, int32_t *idx, float *gate, float *logits_out, float *psum,
+                           void *ws, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status s = moe::validate_groups(cfg, groups);
+    if (s != MOE_OK) return s;
+    return router_impl(cfg, groups, x, Wr, logit_bias, sel_bias, idx, gate, logits_out, psum, ws, ws_bytes, stream);
 }
 
 moe_status moe_permute(const moe_config *cfg, const void *x, const int32_t *idx, const float *gate,
@@ -535,8 +600,9 @@ moe_status moe_balance_stats(const moe_config *cfg, const int32_t *counts, const
 }
 
 // The layer's forward pass; pre / pre_s non-null: the training form, which
-// also leaves the expert pre-activations there (bf16 layers).
-static moe_status forward_impl(const moe_config *cfg, const void *x, const float *Wr, const float *logit_bias,
+// also leaves the expert pre-activations there (bf16 layers); groups non-null:
+// group-limited routing.
+static moe_status forward_impl(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const float *logit_bias,
                                const float *sel_bias, const void *W1, const float *b1, const void *Wu, const void *W2,
                                const float *b2, const void *Wsh_g, const void *Wsh_u, const void *Wsh_d, void *y,
                                int32_t *idx, float *gate, int32_t *counts, float *f, float *P, double *loss,
@@ -568,7 +634,7 @@ static moe_status forward_impl(const moe_config *cfg, const void *x, const float
                        cfg->T, cfg->d_model, cfg->E, cfg->top_k, cfg->score, cfg->renorm,
                        at<char>(ws, L.router_w), at<float>(ws, L.logits), status_word(ws), num_sms()};
     ra.split_ready = bf16 && router_split_ready(ws, Wr, cfg->d_model, cfg->E);
-    if ((e = moe::launch_router(ra, bf16, st)) != cudaSuccess) return cuda_fail(e, "router");
+    if ((e = moe::launch_router_any(ra, bf16, groups, st)) != cudaSuccess) return cuda_fail(e, "router");
 
     moe::DispatchArgs da{};
     da.x = x; da.idx = idx; da.gate = gate;
@@ -607,11 +673,22 @@ moe_status moe_forward(const moe_config *cfg, const void *x, const float *Wr, co
                        const float *b2, const void *Wsh_g, const void *Wsh_u, const void *Wsh_d, void *y,
                        int32_t *idx, float *gate, int32_t *counts, float *f, float *P, double *loss,
                        float *logits_out, int32_t *n_dropped, void *ws, size_t ws_bytes, moe_stream_t stream) {
-    return forward_impl(cfg, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate,
+    return forward_impl(cfg, nullptr, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate,
                         counts, f, P, loss, logits_out, n_dropped, ws, ws_bytes, stream, nullptr, nullptr);
 }
 
-moe_status moe_forward_train(const moe_config *cfg, const void *x, const float *Wr, const float *logit_bias,
+moe_status moe_forward_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const float *logit_bias,
+                       const float *sel_bias, const void *W1, const float *b1, const void *Wu, const void *W2,
+                       const float *b2, const void *Wsh_g, const void *Wsh_u, const void *Wsh_d, void *y,
+                       int32_t *idx, float *gate, int32_t *counts, float *f, float *P, double *loss,
+                       float *logits_out, int32_t *n_dropped, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status s = moe::validate_groups(cfg, groups);
+    if (s != MOE_OK) return s;
+    return forward_impl(cfg, groups, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate,
+                        counts, f, P, loss, logits_out, n_dropped, ws, ws_bytes, stream, nullptr, nullptr);
+}
+
+static moe_status forward_train_impl(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const float *logit_bias,
                              const float *sel_bias, const void *W1, const float *b1, const void *Wu, const void *W2,
                              const float *b2, const void *Wsh_g, const void *Wsh_u, const void *Wsh_d, void *y,
                              int32_t *idx, float *gate, int32_t *counts, float *f, float *P, double *loss,
@@ -628,10 +705,32 @@ moe_status moe_forward_train(const moe_config *cfg, const void *x, const float *
     if (!moe::bwd_preact_buffers(cfg, bwd_ws, &GU, &GUs))
         return fail(MOE_ERR_UNSUPPORTED, "training forward: the layer has no backward pass%s");
     moe::forget_saved_preacts(bwd_ws);
-    s = forward_impl(cfg, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate, counts,
+    s = forward_impl(cfg, groups, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate, counts,
                      f, P, loss, logits_out, n_dropped, ws, ws_bytes, stream, GU, GUs);
     if (s == MOE_OK) moe::note_saved_preacts(bwd_ws, ws, *cfg);
     return s;
+}
+
+moe_status moe_forward_train(const moe_config *cfg, const void *x, const float *Wr, const float *logit_bias,
+                             const float *sel_bias, const void *W1, const float *b1, const void *Wu, const void *W2,
+                             const float *b2, const void *Wsh_g, const void *Wsh_u, const void *Wsh_d, void *y,
+                             int32_t *idx, float *gate, int32_t *counts, float *f, float *P, double *loss,
+                             float *logits_out, int32_t *n_dropped, void *ws, size_t ws_bytes, void *bwd_ws,
+                             size_t bwd_ws_bytes, moe_stream_t stream) {
+    return forward_train_impl(cfg, nullptr, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate,
+                              counts, f, P, loss, logits_out, n_dropped, ws, ws_bytes, bwd_ws, bwd_ws_bytes, stream);
+}
+
+moe_status moe_forward_train_groups(const moe_config *cfg, const moe_route_groups *groups, const void *x, const float *Wr, const float *logit_bias,
+                             const float *sel_bias, const void *W1, const float *b1, const void *Wu, const void *W2,
+                             const float *b2, const void *Wsh_g, const void *Wsh_u, const void *Wsh_d, void *y,
+                             int32_t *idx, float *gate, int32_t *counts, float *f, float *P, double *loss,
+                             float *logits_out, int32_t *n_dropped, void *ws, size_t ws_bytes, void *bwd_ws,
+                             size_t bwd_ws_bytes, moe_stream_t stream) {
+    const moe_status s = moe::validate_groups(cfg, groups);
+    if (s != MOE_OK) return s;
+    return forward_train_impl(cfg, groups, x, Wr, logit_bias, sel_bias, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, y, idx, gate,
+                              counts, f, P, loss, logits_out, n_dropped, ws, ws_bytes, bwd_ws, bwd_ws_bytes, stream);
 }
 
 size_t moe_ep_workspace_size(const moe_config *cfg, int32_t n_src, int64_t max_rows) {
@@ -863,6 +962,164 @@ moe_status moe_forward_fp8(const moe_config *cfg, const void *x, const float *Wr
 
     moe::CombineArgs ca{y_perm, row_of, y, status_word(ws), cfg->T, cfg->d_model, cfg->top_k,
                         cfg->d_ff_shared > 0 ? 1 : 0, (int64_t)cfg->T * cfg->top_k, num_sms(), true};
+    if ((e = moe::launch_combine(ca, true, st)) != cudaSuccess) return cuda_fail(e, "combine");
+    return MOE_OK;
+}
+
+// ---- e4m3 experts with one scale per block of 128
+static moe::FfnFp8BlockArgs fp8_block_args(const moe_config *cfg, const uint8_t *x8_perm, const float *xs_perm,
+                                           const uint8_t *x8, const float *xs, int64_t ld_xs, const int32_t *offsets,
+                                           const float *row_gate, const moe_fp8_block_experts *w, const float *b1,
+                                           const float *b2, void *y_perm, void *ws) {
+    const Layout L = layout(cfg);
+    moe::FfnFp8BlockArgs a{};
+    a.x_perm = x8_perm; a.xs_perm = xs_perm; a.x = x8; a.xs = xs; a.ld_xs = ld_xs;
+    a.offsets = offsets; a.row_gate = row_gate;
+    a.W1 = w->W1; a.W1s = w->W1_scale; a.Wu = w->Wu; a.Wus = w->Wu_scale; a.W2 = w->W2; a.W2s = w->W2_scale;
+    a.Wsg = w->Wsh_g; a.Wsgs = w->Wsh_g_scale; a.Wsu = w->Wsh_u; a.Wsus = w->Wsh_u_scale;
+    a.Wsd = w->Wsh_d; a.Wsds = w->Wsh_d_scale;
+    a.ld_xs_shared = ld_xs;
+    a.sld = w->sld;
+    a.b1 = b1; a.b2 = b2;
+    a.hF = std::max(cfg->d_ff, cfg->d_ff_shared);
+    a.H8 = at<uint8_t>(ws, L.H8);
+    a.h_scale = at<float>(ws, L.hs);
+    a.ld_hs = (int64_t)scale_row_bytes(a.hF);
+    a.y_perm = static_cast<__nv_bfloat16 *>(y_perm);
+    a.status = status_word(ws);
+    a.T = cfg->T; a.d = cfg->d_model; a.E = cfg->E; a.F = cfg->d_ff; a.S = cfg->d_ff_shared; a.act = cfg->act;
+    a.routed_rows = a.shared_base = (int64_t)cfg->T * cfg->top_k;
+    a.num_sms = num_sms();
+    return a;
+}
+
+moe_status moe_quantize_rows_block(const void *in, int64_t rows, int32_t cols, int64_t ld_in, uint8_t *codes,
+                                   int64_t ld_out, float *scale, int64_t ld_scale, moe_stream_t stream) {
+    if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "negative rows or cols%s");
+    if (rows == 0 || cols == 0) return MOE_OK;
+    NEED(in); NEED(codes); NEED(scale);
+    if (cols % 8) return fail(MOE_ERR_UNSUPPORTED, "cols must be a multiple of 8%s");
+    if (ld_in < cols || ld_in % 8) return fail(MOE_ERR_INVALID_ARG, "ld_in < cols or not a multiple of 8%s");
+    if (ld_out < cols || ld_out % 8) return fail(MOE_ERR_INVALID_ARG, "ld_out < cols or not a multiple of 8%s");
+    if (ld_scale < ((int64_t)cols + 127) / 128 * 4 || ld_scale % 4)
+        return fail(MOE_ERR_INVALID_ARG, "ld_scale below 4 * ceil(cols / 128) or not a multiple of 4%s");
+    ALIGNED(in, 16); ALIGNED(codes, 8); ALIGNED(scale, 4);
+    moe::QuantBlockArgs q{};
+    q.in = static_cast<const __nv_bfloat16 *>(in); q.ld_in = ld_in;
+    q.out = codes; q.ld_out = ld_out; q.scale = scale; q.ld_scale = ld_scale;
+    q.rows = rows; q.cols = cols; q.num_sms = num_sms();
+    cudaError_t e = moe::launch_quant_block(q, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "quantize_rows_block");
+}
+
+moe_status moe_grouped_ffn_fp8_block(const moe_config *cfg, const uint8_t *x8_perm, const float *xs_perm,
+                                     const int32_t *offsets, const float *row_gate, const moe_fp8_block_experts *w,
+                                     const float *b1, const float *b2, const uint8_t *x8, const float *xs,
+                                     void *y_perm, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    moe_status s = check_cfg(cfg);
+    if (s != MOE_OK) return s;
+    NEED(w);
+    if ((s = check_fp8_block_cfg(cfg, w->sld)) != MOE_OK) return s;
+    if (cfg->T > 0) {
+        NEED(x8_perm); NEED(xs_perm); NEED(offsets); NEED(row_gate); NEED(y_perm);
+        if ((s = check_fp8_block_weights(cfg, w)) != MOE_OK) return s;
+        if (cfg->d_ff_shared > 0) { NEED(x8); NEED(xs); }
+    }
+    ALIGNED(x8_perm, 16); ALIGNED(x8, 16); ALIGNED(y_perm, 16); ALIGNED(xs_perm, 16); ALIGNED(xs, 16);
+    ALIGNED(offsets, 4); ALIGNED(row_gate, 4); ALIGNED(b1, 4); ALIGNED(b2, 4);
+    if ((s = check_ws(cfg, ws, ws_bytes)) != MOE_OK) return s;
+    moe::forget_saved_preacts(ws);        // the packed rows / hidden activation change
+    if (cfg->T == 0) return MOE_OK;
+    moe::FfnFp8BlockArgs a = fp8_block_args(cfg, x8_perm, xs_perm, x8, xs, w->sld, offsets, row_gate, w, b1, b2,
+                                            y_perm, ws);
+    cudaError_t e = moe::launch_ffn_fp8_block(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped_ffn_fp8_block");
+}
+
+moe_status moe_forward_fp8_block(const moe_config *cfg, const moe_route_groups *groups, const void *x,
+                                 const uint8_t *x8, const float *xs, const float *Wr, const float *logit_bias,
+                                 const float *sel_bias, const moe_fp8_block_experts *w, const float *b1,
+                                 const float *b2, void *y, int32_t *idx, float *gate, int32_t *counts, float *f,
+                                 float *P, double *loss, float *logits_out, int32_t *n_dropped, void *ws,
+                                 size_t ws_bytes, moe_stream_t stream) {
+    moe_status s = check_cfg(cfg);
+    if (s != MOE_OK) return s;
+    if (groups && (s = check_groups(cfg, groups)) != MOE_OK) return s;
+    NEED(counts); NEED(f); NEED(P); NEED(loss); NEED(w);
+    if ((s = check_fp8_block_cfg(cfg, w->sld)) != MOE_OK) return s;
+    if (cfg->T > 0) {
+        NEED(x); NEED(Wr); NEED(y); NEED(idx); NEED(gate);
+        if ((s = check_fp8_block_weights(cfg, w)) != MOE_OK) return s;
+        if ((x8 == nullptr) != (xs == nullptr)) return fail(MOE_ERR_INVALID_ARG, "x8 and xs: both or neither%s");
+    }
+    ALIGNED(x, 16); ALIGNED(y, 16); ALIGNED(Wr, 4); ALIGNED(logit_bias, 4); ALIGNED(sel_bias, 4); ALIGNED(x8, 16);
+    ALIGNED(xs, 16); ALIGNED(b1, 4); ALIGNED(b2, 4); ALIGNED(idx, 4); ALIGNED(gate, 4); ALIGNED(counts, 4);
+    ALIGNED(f, 4); ALIGNED(P, 4); ALIGNED(loss, 8); ALIGNED(logits_out, 4); ALIGNED(n_dropped, 4);
+    if ((s = check_ws(cfg, ws, ws_bytes)) != MOE_OK) return s;
+    moe::forget_saved_preacts(ws);        // the packed rows / hidden activation change
+    const Layout L = layout(cfg);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t rows = (int64_t)cfg->T * cfg->top_k;
+    float *psum = at<float>(ws, L.psum);
+    int32_t *offsets = at<int32_t>(ws, L.offsets);
+    float *xs_perm = at<float>(ws, L.xs_perm);
+    cudaError_t e;
+
+    moe::RouterArgs ra{x, Wr, logit_bias, sel_bias, idx, gate, logits_out, psum,
+                       cfg->T, cfg->d_model, cfg->E, cfg->top_k, cfg->score, cfg->renorm,
+                       at<char>(ws, L.router_w), at<float>(ws, L.logits), status_word(ws), num_sms()};
+    ra.split_ready = router_split_ready(ws, Wr, cfg->d_model, cfg->E);
+    if ((e = moe::launch_router_any(ra, true, groups, st)) != cudaSuccess) return cuda_fail(e, "router");
+
+    // x's codes and scale rows: the caller's, or quantized here.  Inside the
+    // workspace the scale rows are ld bytes apart, the caller's w->sld.
+    const int64_t ld = (int64_t)scale_row_bytes(cfg->d_model);
+    int64_t ld_xs = w->sld;
+    if (x8 == nullptr) {
+        moe::QuantBlockArgs q{};
+        q.in = static_cast<const __nv_bfloat16 *>(x); q.ld_in = cfg->d_model;
+        q.out = at<uint8_t>(ws, L.x8); q.ld_out = cfg->d_model;
+        q.scale = at<float>(ws, L.xs); q.ld_scale = ld;
+        q.rows = cfg->T; q.cols = cfg->d_model; q.num_sms = num_sms();
+        q.pdl = true;
+        if ((e = moe::launch_quant_block(q, st)) != cudaSuccess) return cuda_fail(e, "quantize_x");
+        x8 = q.out;
+        xs = q.scale;
+        ld_xs = ld;
+    }
+
+    moe::DispatchArgs da{};
+    da.x = x8; da.idx = idx; da.gate = gate;
+    da.chunk_cnt = at<int32_t>(ws, L.chunk_cnt);
+    da.chunk_base = at<int32_t>(ws, L.chunk_base);
+    da.counts = counts; da.kept = at<int32_t>(ws, L.kept); da.offsets = offsets;
+    da.row_of = at<int32_t>(ws, L.row_of); da.row_token = at<int32_t>(ws, L.row_token);
+    da.row_gate = at<float>(ws, L.row_gate);
+    da.x_perm = at<char>(ws, L.x_perm);
+    da.n_dropped = n_dropped;
+    da.status = status_word(ws);
+    da.T = cfg->T; da.d = cfg->d_model; da.E = cfg->E; da.k = cfg->top_k;
+    da.capacity = moe_capacity(cfg);
+    da.psum = psum; da.f = f; da.P = P; da.loss = loss;
+    da.contrib = at<double>(ws, L.contrib);
+    da.nblk = moe::router_blocks(cfg->T, true);
+    da.pdl = true;
+    if ((e = moe::launch_dispatch(da, 1, st)) != cudaSuccess) return cuda_fail(e, "permute");
+    if (cfg->T == 0) return MOE_OK;
+
+    // the packed rows' scale rows follow their codes
+    if ((e = moe::launch_gather_scales(xs, ld_xs, xs_perm, ld, (cfg->d_model + 127) / 128, da.row_token,
+                                       offsets + cfg->E, rows, num_sms(), st)) != cudaSuccess)
+        return cuda_fail(e, "gather_scales");
+
+    moe::FfnFp8BlockArgs fa = fp8_block_args(cfg, static_cast<const uint8_t *>(da.x_perm), xs_perm, x8, xs, ld, offsets,
+                                             da.row_gate, w, b1, b2, at<char>(ws, L.y_perm), ws);
+    fa.ld_xs_shared = ld_xs;
+    fa.pdl = true;
+    if ((e = moe::launch_ffn_fp8_block(fa, st)) != cudaSuccess) return cuda_fail(e, "grouped_ffn_fp8_block");
+
+    moe::CombineArgs ca{fa.y_perm, da.row_of, y, status_word(ws), cfg->T, cfg->d_model, cfg->top_k,
+                        cfg->d_ff_shared > 0 ? 1 : 0, rows, num_sms(), true};
     if ((e = moe::launch_combine(ca, true, st)) != cudaSuccess) return cuda_fail(e, "combine");
     return MOE_OK;
 }

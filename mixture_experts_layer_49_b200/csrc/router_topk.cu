@@ -343,4 +343,34 @@ cudaError_t launch_router(const RouterArgs &a, bool bf16, cudaStream_t st) {
     return launch_kernel(router_select_kernel<8>, blocks, threads, 0, st, true, a, cparts, splits);
 }
 
+// Group-limited selection: the same logits, then route_groups.cu.  fp32 layers
+// take their logits from the FFMA kernel, whose own selection is overwritten.
+cudaError_t launch_router_any(const RouterArgs &a, bool bf16, const moe_route_groups *groups, cudaStream_t st) {
+    if (groups == nullptr) return launch_router(a, bf16, st);
+    if (a.T == 0) return cudaSuccess;
+    RouteArgs r{};
+    float *parts = a.logits_out ? a.logits_out : a.logits_ws;
+    r.splits = 1;
+    cudaError_t e;
+    if (bf16) {
+        r.splits = router_logit_splits(a.T, a.d, a.num_sms);
+        if (r.splits > 1) parts = a.logits_ws;
+        e = launch_router_logits_tc(a, parts, r.splits, st);
+    } else {
+        RouterArgs f = a;
+        f.logits_out = parts;
+        e = launch_router_t<float>(f, st);
+    }
+    if (e != cudaSuccess) return e;
+    r.logits = parts;
+    r.sel_bias = a.sel_bias;
+    r.logits_out = r.splits > 1 ? a.logits_out : nullptr;
+    r.idx = a.idx; r.gate = a.gate; r.psum = a.psum;
+    r.T = a.T; r.E = a.E; r.k = a.k; r.score = a.score; r.renorm = a.renorm;
+    r.n_group = groups->n_group; r.topk_group = groups->topk_group; r.group_top = groups->group_top;
+    r.gate_scale = groups->gate_scale;
+    r.pdl = true;
+    return launch_route_select(r, st);
+}
+
 }  // namespace moe

@@ -33,7 +33,11 @@ EXPORTS = ("moe_workspace_size", "moe_capacity", "moe_router_blocks", "moe_perm_
            "moe_ep_workspace_size", "moe_ep_grouped_ffn", "moe_backward_workspace_size", "moe_backward",
            "moe_forward_train",
            "moe_quantize_rows_mx", "moe_grouped_ffn_mx_workspace_size", "moe_grouped_ffn_mx",
-           "moe_router_freeze", "moe_forward_mx", "moe_grouped_ffn_w4", "moe_forward_w4")
+           "moe_router_freeze", "moe_forward_mx", "moe_grouped_ffn_w4", "moe_forward_w4",
+           "moe_quantize_rows_block", "moe_grouped_ffn_fp8_block", "moe_forward_fp8_block",
+           "moe_route_select", "moe_route_backward", "moe_router_topk_groups", "moe_forward_groups",
+           "moe_forward_train_groups", "moe_backward_groups", "moe_rmsnorm", "moe_rmsnorm_backward",
+           "moe_rmsnorm_backward_workspace_size")
 
 
 class MoeFp8Experts(ctypes.Structure):
@@ -58,6 +62,19 @@ class MoeW4Experts(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "W1", "W1_scale", "Wu", "Wu_scale", "W2", "W2_scale",
         "Wsh_g", "Wsh_g_scale", "Wsh_u", "Wsh_u_scale", "Wsh_d", "Wsh_d_scale")] + [("sld", ctypes.c_int32)]
+
+
+class MoeFp8BlockExperts(ctypes.Structure):
+    """moe_fp8_block_experts: e4m3 expert weights (device pointers), their fp32
+    scales per 128 x 128 block and the scale row stride sld."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "W1", "W1_scale", "Wu", "Wu_scale", "W2", "W2_scale",
+        "Wsh_g", "Wsh_g_scale", "Wsh_u", "Wsh_u_scale", "Wsh_d", "Wsh_d_scale")] + [("sld", ctypes.c_int32)]
+
+
+class MoeRouteGroups(ctypes.Structure):
+    """moe_route_groups: group-limited routing (see include/moe.h)."""
+    _fields_ = [("n_group", c_i32), ("topk_group", c_i32), ("group_top", c_i32), ("gate_scale", ctypes.c_float)]
 
 
 class MoeWsView(ctypes.Structure):
@@ -168,6 +185,29 @@ def lib():
         L.moe_forward_fp8.restype = ctypes.c_int
         L.moe_forward_fp8.argtypes = [P(MoeConfig)] + [c_vp] * 4 + [P(MoeFp8Experts)] + [c_vp] * 12 + [
             ctypes.c_size_t, c_vp]
+        G = P(MoeRouteGroups)
+        for name, args in (
+                ("moe_quantize_rows_block", [c_vp, ctypes.c_int64, c_i32, ctypes.c_int64, c_vp, ctypes.c_int64, c_vp,
+                                             ctypes.c_int64, c_vp]),
+                ("moe_grouped_ffn_fp8_block", [P(MoeConfig)] + [c_vp] * 4 + [P(MoeFp8BlockExperts)] + [c_vp] * 6 + [
+                    ctypes.c_size_t, c_vp]),
+                ("moe_forward_fp8_block", [P(MoeConfig), G] + [c_vp] * 6 + [P(MoeFp8BlockExperts)] + [c_vp] * 12 + [
+                    ctypes.c_size_t, c_vp]),
+                ("moe_route_select", [P(MoeConfig), G] + [c_vp] * 6),
+                ("moe_route_backward", [P(MoeConfig), G] + [c_vp] * 4 + [ctypes.c_float, c_vp, c_vp]),
+                ("moe_router_topk_groups", [P(MoeConfig), G] + L.moe_router_topk.argtypes[1:]),
+                ("moe_forward_groups", [P(MoeConfig), G] + L.moe_forward.argtypes[1:]),
+                ("moe_forward_train_groups", [P(MoeConfig), G] + L.moe_forward_train.argtypes[1:]),
+                ("moe_backward_groups", [P(MoeConfig), G] + L.moe_backward.argtypes[1:]),
+                ("moe_rmsnorm", [c_i32, ctypes.c_int64, c_i32, c_vp, c_vp, c_vp, ctypes.c_float, c_vp, c_vp, c_vp, c_vp,
+                                 ctypes.c_int64, c_vp]),
+                ("moe_rmsnorm_backward", [c_i32, ctypes.c_int64, c_i32, c_vp, c_vp, ctypes.c_float, c_vp, c_vp, c_vp,
+                                          c_vp, c_vp, ctypes.c_size_t, c_vp])):
+            f = getattr(L, name)
+            f.restype = ctypes.c_int
+            f.argtypes = args
+        L.moe_rmsnorm_backward_workspace_size.restype = ctypes.c_size_t
+        L.moe_rmsnorm_backward_workspace_size.argtypes = [ctypes.c_int64, c_i32]
         _lib = L
     return _lib
 
@@ -339,10 +379,22 @@ def moe_backward(cfg, x, Wr, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, idx, gate,
                               _stream(stream)), "moe_backward")
 
 
-def backward(cfg, inp, out, fwd_ws, dy, alpha=0.0, ws=None, stream=None) -> dict:
+def moe_backward_groups(cfg, groups, x, Wr, W1, b1, Wu, W2, b2, Wsh_g, Wsh_u, Wsh_d, idx, gate, logits, counts, dy,
+                        alpha, dx, dWr, dlogit_bias, dW1, db1, dWu, dW2, db2, dWsh_g, dWsh_u, dWsh_d, fwd_ws, ws,
+                        stream=None):
+    _check(lib().moe_backward_groups(ctypes.byref(cfg), ctypes.byref(groups), _p(x), _p(Wr), _p(W1), _p(b1), _p(Wu),
+                                     _p(W2), _p(b2), _p(Wsh_g), _p(Wsh_u), _p(Wsh_d), _p(idx), _p(gate), _p(logits),
+                                     _p(counts), _p(dy), float(alpha), _p(dx), _p(dWr), _p(dlogit_bias), _p(dW1),
+                                     _p(db1), _p(dWu), _p(dW2), _p(db2), _p(dWsh_g), _p(dWsh_u), _p(dWsh_d),
+                                     _p(fwd_ws), fwd_ws.numel(), _p(ws), ws.numel(), _stream(stream)),
+           "moe_backward_groups")
+
+
+def backward(cfg, inp, out, fwd_ws, dy, alpha=0.0, ws=None, stream=None, groups=None) -> dict:
     """moe_backward after forward(cfg, inp, out, fwd_ws) (out must hold the
     router logits: Outputs(..., want_logits=True)).  Returns the gradients
-    as fp32 tensors (dx in the layer dtype) keyed like the inputs."""
+    as fp32 tensors (dx in the layer dtype) keyed like the inputs.  groups:
+    the forward pass's (moe_backward_groups)."""
     if out.logits is None:
         raise ValueError("the backward pass needs the forward's router logits (Outputs(want_logits=True))")
     dev = dy.device
@@ -357,10 +409,14 @@ def backward(cfg, inp, out, fwd_ws, dy, alpha=0.0, ws=None, stream=None) -> dict
              dWsd=torch.empty((d, S), **f32) if S else None)
     if ws is None:
         ws = torch.empty(backward_workspace_size(cfg), dtype=torch.uint8, device=dev)
-    moe_backward(cfg, inp["x"], inp["Wr"], inp["W1"], inp.get("b1"), inp.get("Wu"), inp["W2"], inp.get("b2"),
-                 inp.get("Wsg"), inp.get("Wsu"), inp.get("Wsd"), out.idx, out.gate, out.logits, out.counts, dy, alpha,
-                 g["dx"], g["dWr"], g["dlogit_bias"], g["dW1"], g["db1"], g["dWu"], g["dW2"], g["db2"], g["dWsg"],
-                 g["dWsu"], g["dWsd"], fwd_ws, ws, stream)
+    args = (inp["x"], inp["Wr"], inp["W1"], inp.get("b1"), inp.get("Wu"), inp["W2"], inp.get("b2"),
+            inp.get("Wsg"), inp.get("Wsu"), inp.get("Wsd"), out.idx, out.gate, out.logits, out.counts, dy, alpha,
+            g["dx"], g["dWr"], g["dlogit_bias"], g["dW1"], g["db1"], g["dWu"], g["dW2"], g["db2"], g["dWsg"],
+            g["dWsu"], g["dWsd"], fwd_ws, ws, stream)
+    if groups is None:
+        moe_backward(cfg, *args)
+    else:
+        moe_backward_groups(cfg, groups, *args)
     return g
 
 
@@ -439,27 +495,49 @@ class Outputs:
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device) if want_logits else None
 
 
-def forward(cfg, inp, out: Outputs, ws, stream=None):
-    """moe_forward on a dict of device inputs (keys as in synthetic.generate)."""
-    moe_forward(cfg, inp["x"], inp["Wr"], inp.get("logit_bias"), inp.get("sel_bias"),
-                inp["W1"], inp.get("b1"), inp.get("Wu"), inp["W2"], inp.get("b2"),
-                inp.get("Wsg"), inp.get("Wsu"), inp.get("Wsd"),
-                out.y, out.idx, out.gate, out.counts, out.f, out.P, out.loss, out.logits,
-                out.n_dropped, ws, stream)
+def _forward_args(inp, out):
+    return (inp["x"], inp["Wr"], inp.get("logit_bias"), inp.get("sel_bias"),
+            inp["W1"], inp.get("b1"), inp.get("Wu"), inp["W2"], inp.get("b2"),
+            inp.get("Wsg"), inp.get("Wsu"), inp.get("Wsd"),
+            out.y, out.idx, out.gate, out.counts, out.f, out.P, out.loss, out.logits, out.n_dropped)
+
+
+def moe_forward_groups(cfg, groups, *args, stream=None):
+    """moe_forward with group-limited routing: its arguments after cfg, up to
+    and including ws."""
+    *tensors, ws = args
+    _check(lib().moe_forward_groups(ctypes.byref(cfg), ctypes.byref(groups), *map(_p, tensors), _p(ws), ws.numel(),
+                                    _stream(stream)), "moe_forward_groups")
+
+
+def moe_forward_train_groups(cfg, groups, *args, stream=None):
+    """moe_forward_train with group-limited routing: its arguments after cfg, up
+    to and including ws and bwd_ws."""
+    *tensors, ws, bwd_ws = args
+    _check(lib().moe_forward_train_groups(ctypes.byref(cfg), ctypes.byref(groups), *map(_p, tensors), _p(ws), ws.numel(),
+                                          _p(bwd_ws), bwd_ws.numel(), _stream(stream)), "moe_forward_train_groups")
+
+
+def forward(cfg, inp, out: Outputs, ws, stream=None, groups=None):
+    """moe_forward on a dict of device inputs (keys as in synthetic.generate);
+    with groups (route_groups), moe_forward_groups."""
+    if groups is None:
+        moe_forward(cfg, *_forward_args(inp, out), ws, stream)
+    else:
+        moe_forward_groups(cfg, groups, *_forward_args(inp, out), ws, stream=stream)
 
 
 def alloc_backward_workspace(cfg, device="cuda") -> torch.Tensor:
     return torch.empty(backward_workspace_size(cfg), dtype=torch.uint8, device=device)
 
 
-def forward_train(cfg, inp, out: Outputs, ws, bwd_ws, stream=None):
+def forward_train(cfg, inp, out: Outputs, ws, bwd_ws, stream=None, groups=None):
     """moe_forward_train: forward(...) that also leaves the expert
     pre-activations in bwd_ws for the following backward(..., ws=bwd_ws)."""
-    moe_forward_train(cfg, inp["x"], inp["Wr"], inp.get("logit_bias"), inp.get("sel_bias"),
-                      inp["W1"], inp.get("b1"), inp.get("Wu"), inp["W2"], inp.get("b2"),
-                      inp.get("Wsg"), inp.get("Wsu"), inp.get("Wsd"),
-                      out.y, out.idx, out.gate, out.counts, out.f, out.P, out.loss, out.logits,
-                      out.n_dropped, ws, bwd_ws, stream)
+    if groups is None:
+        moe_forward_train(cfg, *_forward_args(inp, out), ws, bwd_ws, stream)
+    else:
+        moe_forward_train_groups(cfg, groups, *_forward_args(inp, out), ws, bwd_ws, stream=stream)
 
 
 # ---------------------------------------------------------------- FP8 experts
@@ -629,3 +707,219 @@ def forward_fp8(cfg, inp, w8, out: Outputs, ws, stream=None):
     moe_forward_fp8(cfg, inp["x"], inp["Wr"], inp.get("logit_bias"), inp.get("sel_bias"), w8,
                     inp.get("b1"), inp.get("b2"), out.y, out.idx, out.gate, out.counts, out.f, out.P, out.loss,
                     out.logits, out.n_dropped, ws, stream)
+
+
+# ---------------------------------------------------------------- experts in e4m3 with a scale per block of 128
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _current_device() -> int:
+    if not torch.cuda.is_available():
+        raise ValueError("libmoe takes device tensors; there is no CUDA device")
+    return torch.cuda.current_device()
+
+
+def _arg(t, name, dev, dtypes, numel=None):
+    """Device pointer of an argument (None -> NULL): a contiguous tensor of one
+    of `dtypes` on the current device, holding at least `numel` elements."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s: libmoe takes device tensors; got one on %s" % (name, t.device))
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), dev))
+    if t.dtype is not dtypes and (not isinstance(dtypes, tuple) or t.dtype not in dtypes):
+        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtypes))
+    if not t.is_contiguous():
+        raise ValueError("%s: libmoe takes contiguous tensors" % name)
+    if numel is not None and t.numel() < numel:
+        raise ValueError("%s holds %d elements, %d are needed" % (name, t.numel(), numel))
+    return t.data_ptr()
+
+
+def _cu_stream(stream, dev):
+    """The stream's handle: the current one, or one of the current device."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device_index != dev:
+        raise ValueError("the stream is on cuda:%d, the current device is cuda:%d" % (stream.device_index, dev))
+    return stream.cuda_stream
+
+
+def fp8_block_sld(cfg) -> int:
+    """Smallest valid scale row stride (bytes) for a configuration."""
+    need = 4 * ((max(cfg.d_model, cfg.d_ff, cfg.d_ff_shared) + 127) // 128)
+    return (need + 15) // 16 * 16
+
+
+def fp8_block_experts(w, sld) -> MoeFp8BlockExperts:
+    """moe_fp8_block_experts from a dict of device tensors: e4m3 codes (uint8 or
+    float8_e4m3fn) under W1, Wu, W2, Wsg, Wsu, Wsd and fp32 scales in rows of sld
+    bytes under "<name>_scale".  The struct may be kept and passed wherever a
+    call takes the experts; it keeps the tensors alive."""
+    dev = _current_device()
+    s = MoeFp8BlockExperts()
+    s._tensors = []
+    for name in FP8_WEIGHTS:
+        field = _FP8_FIELD[name]
+        codes, scale = w.get(name), w.get(name + "_scale")
+        rows = 0 if codes is None else codes.numel() // max(1, codes.shape[-1] * codes.shape[-2])
+        blocks = 0 if codes is None else rows * ((codes.shape[-2] + 127) // 128)
+        setattr(s, field, _arg(codes, name, dev, _CODES))
+        setattr(s, field + "_scale", _arg(scale, name + "_scale", dev, _F32, blocks * int(sld) // 4))
+        s._tensors += [codes, scale]
+    s.sld = int(sld)
+    return s
+
+
+def _block_experts(w, sld=None) -> MoeFp8BlockExperts:
+    return w if isinstance(w, MoeFp8BlockExperts) else fp8_block_experts(w, sld)
+
+
+def moe_quantize_rows_block(x, codes, scale, rows=None, cols=None, ld_in=None, ld_out=None, ld_scale=None,
+                            stream=None):
+    """1 x 128 quantization of a bf16 [rows, cols] tensor into codes (uint8 or
+    float8_e4m3fn) and fp32 scales [rows, >= ceil(cols / 128)] (ld_scale: bytes
+    between their rows)."""
+    dev = _current_device()
+    rows = x.shape[0] if rows is None else rows
+    cols = x.shape[1] if cols is None else cols
+    ld_in = x.shape[1] if ld_in is None else ld_in
+    ld_out = codes.shape[1] if ld_out is None else ld_out
+    ld_scale = scale.shape[1] * 4 if ld_scale is None else ld_scale
+    last = max(rows - 1, 0)
+    _check(lib().moe_quantize_rows_block(
+        _arg(x, "x", dev, _BF16, last * ld_in + cols if rows else 0), rows, cols, ld_in,
+        _arg(codes, "codes", dev, _CODES, last * ld_out + cols if rows else 0), ld_out,
+        _arg(scale, "scale", dev, _F32, last * ld_scale // 4 + (cols + 127) // 128 if rows else 0), ld_scale,
+        _cu_stream(stream, dev)), "moe_quantize_rows_block")
+
+
+def moe_grouped_ffn_fp8_block(cfg, x8_perm, xs_perm, offsets, row_gate, w, b1, b2, x8, xs, y_perm, ws, stream=None):
+    """moe_grouped_ffn_fp8_block; w: fp8_block_experts(...)."""
+    dev = _current_device()
+    T, d, E = cfg.T, cfg.d_model, cfg.E
+    rows, spr = T * cfg.top_k, w.sld // 4
+    _check(lib().moe_grouped_ffn_fp8_block(
+        ctypes.byref(cfg), _arg(x8_perm, "x8_perm", dev, _CODES, rows * d),
+        _arg(xs_perm, "xs_perm", dev, _F32, rows * spr), _arg(offsets, "offsets", dev, _I32, E + 1),
+        _arg(row_gate, "row_gate", dev, _F32, rows), ctypes.byref(w), _arg(b1, "b1", dev, _F32, E * cfg.d_ff),
+        _arg(b2, "b2", dev, _F32, E * d), _arg(x8, "x8", dev, _CODES, T * d), _arg(xs, "xs", dev, _F32, T * spr),
+        _arg(y_perm, "y_perm", dev, _BF16, (rows + (T if cfg.d_ff_shared else 0)) * d),
+        _arg(ws, "ws", dev, torch.uint8), ws.numel(), _cu_stream(stream, dev)), "moe_grouped_ffn_fp8_block")
+
+
+def moe_forward_fp8_block(cfg, groups, x, x8, xs, Wr, logit_bias, sel_bias, w, b1, b2, y, idx, gate, counts, f, P,
+                          loss, logits_out, n_dropped, ws, stream=None):
+    """moe_forward_fp8_block; groups may be None, x8 and xs may both be None."""
+    dev = _current_device()
+    T, d, E, k = cfg.T, cfg.d_model, cfg.E, cfg.top_k
+    _check(lib().moe_forward_fp8_block(
+        ctypes.byref(cfg), None if groups is None else ctypes.byref(groups), _arg(x, "x", dev, _BF16, T * d),
+        _arg(x8, "x8", dev, _CODES, T * d), _arg(xs, "xs", dev, _F32, T * (w.sld // 4)),
+        _arg(Wr, "Wr", dev, _F32, d * E), _arg(logit_bias, "logit_bias", dev, _F32, E),
+        _arg(sel_bias, "sel_bias", dev, _F32, E), ctypes.byref(w), _arg(b1, "b1", dev, _F32, E * cfg.d_ff),
+        _arg(b2, "b2", dev, _F32, E * d), _arg(y, "y", dev, _BF16, T * d), _arg(idx, "idx", dev, _I32, T * k),
+        _arg(gate, "gate", dev, _F32, T * k), _arg(counts, "counts", dev, _I32, E), _arg(f, "f", dev, _F32, E),
+        _arg(P, "P", dev, _F32, E), _arg(loss, "loss", dev, torch.float64, 1),
+        _arg(logits_out, "logits_out", dev, _F32, T * E), _arg(n_dropped, "n_dropped", dev, _I32, 1),
+        _arg(ws, "ws", dev, torch.uint8), ws.numel(), _cu_stream(stream, dev)), "moe_forward_fp8_block")
+
+
+def forward_fp8_block(cfg, inp, w, sld, out: Outputs, ws, stream=None, groups=None, x8=None, xs=None):
+    """moe_forward_fp8_block on a dict of device inputs and block-scaled experts
+    (a dict of tensors, or fp8_block_experts(...)); x8, xs: x's codes and scale
+    rows where moe_rmsnorm has written them."""
+    moe_forward_fp8_block(cfg, groups, inp["x"], x8, xs, inp["Wr"], inp.get("logit_bias"), inp.get("sel_bias"),
+                          _block_experts(w, sld), inp.get("b1"), inp.get("b2"), out.y, out.idx, out.gate, out.counts,
+                          out.f, out.P, out.loss, out.logits, out.n_dropped, ws, stream)
+
+
+# ---------------------------------------------------------------- group-limited routing
+def route_groups(n_group, topk_group, group_top=2, gate_scale=1.0) -> MoeRouteGroups:
+    """moe_route_groups: topk_group of n_group groups by the sum of their
+    group_top largest keys; gates times gate_scale."""
+    return MoeRouteGroups(int(n_group), int(topk_group), int(group_top), float(gate_scale))
+
+
+def moe_route_select(cfg, groups, logits, sel_bias, idx, gate, psum=None, stream=None):
+    """Group-limited selection from logits [T, E] fp32."""
+    dev = _current_device()
+    T, E, k = cfg.T, cfg.E, cfg.top_k
+    _check(lib().moe_route_select(
+        ctypes.byref(cfg), ctypes.byref(groups), _arg(logits, "logits", dev, _F32, T * E),
+        _arg(sel_bias, "sel_bias", dev, _F32, E), _arg(idx, "idx", dev, _I32, T * k),
+        _arg(gate, "gate", dev, _F32, T * k), _arg(psum, "psum", dev, _F32, (T + 31) // 32 * E),
+        _cu_stream(stream, dev)), "moe_route_select")
+
+
+def moe_route_backward(cfg, groups, logits, idx, dgate, counts, alpha, dlogits, stream=None):
+    """Gradient of moe_route_select's gates (and alpha times the balance loss)
+    with respect to the logits."""
+    dev = _current_device()
+    T, E, k = cfg.T, cfg.E, cfg.top_k
+    _check(lib().moe_route_backward(
+        ctypes.byref(cfg), ctypes.byref(groups), _arg(logits, "logits", dev, _F32, T * E),
+        _arg(idx, "idx", dev, _I32, T * k), _arg(dgate, "dgate", dev, _F32, T * k),
+        _arg(counts, "counts", dev, _I32, E), float(alpha), _arg(dlogits, "dlogits", dev, _F32, T * E),
+        _cu_stream(stream, dev)), "moe_route_backward")
+
+
+def moe_router_topk_groups(cfg, groups, x, Wr, logit_bias, sel_bias, idx, gate, logits_out, psum, ws, stream=None):
+    _check(lib().moe_router_topk_groups(ctypes.byref(cfg), ctypes.byref(groups), _p(x), _p(Wr), _p(logit_bias),
+                                        _p(sel_bias), _p(idx), _p(gate), _p(logits_out), _p(psum), _p(ws), ws.numel(),
+                                        _stream(stream)), "moe_router_topk_groups")
+
+
+# ---------------------------------------------------------------- RMS norm
+def _norm_dtype(t):
+    if t.dtype is _BF16:
+        return MOE_BF16
+    if t.dtype is _F32:
+        return MOE_F32
+    raise ValueError("RMS norm takes bf16 or fp32 rows, got %s" % t.dtype)
+
+
+def moe_rmsnorm(x, residual, weight, eps, h, y, codes=None, scale=None, stream=None):
+    """RMS norm of x + residual ([rows, d] bf16 or fp32; residual may be None)
+    into y, the sum into h, and the norm's 1 x 128 quantization into codes (uint8
+    or float8_e4m3fn [rows, d]) and scale (fp32 [rows, >= ceil(d / 128)]).  h, y,
+    and codes with scale may each be None."""
+    dev = _current_device()
+    rows, d = x.shape
+    dt, n = x.dtype, rows * d
+    ld = 0
+    if scale is not None:
+        ld = scale.shape[-1] * 4
+    _check(lib().moe_rmsnorm(
+        _norm_dtype(x), rows, d, _arg(x, "x", dev, dt), _arg(residual, "residual", dev, dt, n),
+        _arg(weight, "weight", dev, _F32, d), eps, _arg(h, "h", dev, dt, n), _arg(y, "y", dev, dt, n),
+        _arg(codes, "codes", dev, _CODES, n), _arg(scale, "scale", dev, _F32, rows * (ld // 4)), ld,
+        _cu_stream(stream, dev)), "moe_rmsnorm")
+
+
+def rmsnorm_backward_workspace_size(rows, d) -> int:
+    n = int(lib().moe_rmsnorm_backward_workspace_size(int(rows), int(d)))
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_rmsnorm_backward_workspace_size", last_error_detail())
+    return n
+
+
+def alloc_rmsnorm_backward_workspace(rows, d, device="cuda") -> torch.Tensor:
+    return torch.empty(rmsnorm_backward_workspace_size(rows, d), dtype=torch.uint8, device=device)
+
+
+def moe_rmsnorm_backward(h, weight, eps, dy, dres, dh, dweight, ws, stream=None):
+    """Gradient of moe_rmsnorm at the stored h: dh (for x and residual alike;
+    dres, the gradient from the residual stream, may be None) and dweight fp32."""
+    dev = _current_device()
+    rows, d = h.shape
+    dt, n = h.dtype, rows * d
+    _check(lib().moe_rmsnorm_backward(
+        _norm_dtype(h), rows, d, _arg(h, "h", dev, dt), _arg(weight, "weight", dev, _F32, d), eps,
+        _arg(dy, "dy", dev, dt, n), _arg(dres, "dres", dev, dt, n), _arg(dh, "dh", dev, dt, n),
+        _arg(dweight, "dweight", dev, _F32, d), _arg(ws, "ws", dev, torch.uint8), ws.numel(),
+        _cu_stream(stream, dev)), "moe_rmsnorm_backward")

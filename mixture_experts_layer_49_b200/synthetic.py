@@ -310,3 +310,37 @@ def generate_fp8_experts(wl: Workload, device="cpu", seed: int = 0) -> dict:
             c, s = _fp8_stack(wl, "Wsu", 1, S, d, dev, seed)
             w["Wsu"], w["Wsu_scale"] = c[0], s[0]
     return w
+
+
+def _fp8_block_stack(wl, name, E, rows, cols, sld, device, seed):
+    codes = torch.empty((E, rows, cols), dtype=torch.uint8, device=device)
+    scales = torch.zeros((E, (rows + 127) // 128, sld // 4), dtype=torch.float32, device=device)
+    nb = (cols + 127) // 128
+    for e in range(E):
+        g = _gen(device, seed, wl, name + "_fp8_block", e)
+        w = torch.randn((rows, cols), generator=g, device=device, dtype=torch.float32)
+        codes[e] = w.to(torch.float8_e4m3fn).view(torch.uint8)
+        scales[e, :, :nb] = (torch.rand((scales.shape[1], nb), generator=g, device=device) + 0.5) / math.sqrt(cols)
+    return codes, scales
+
+
+def generate_fp8_block_experts(wl: Workload, sld: int, device="cpu", seed: int = 0) -> dict:
+    """Expert weights in e4m3 with one fp32 scale per 128 x 128 block: codes of
+    N(0, 1) draws, scales from U(0.5, 1.5) / sqrt(fan_in) in rows of sld bytes
+    (zeros behind the last block).  Keys as in generate_fp8_experts; GELU
+    biases b1, b2 as in generate."""
+    dev = torch.device(device)
+    E, F, d, S = wl.E, wl.d_ff, wl.d_model, wl.d_ff_shared
+    w = {}
+    w["W1"], w["W1_scale"] = _fp8_block_stack(wl, "W1", E, F, d, sld, dev, seed)
+    w["W2"], w["W2_scale"] = _fp8_block_stack(wl, "W2", E, d, F, sld, dev, seed)
+    if wl.act == "swiglu":
+        w["Wu"], w["Wu_scale"] = _fp8_block_stack(wl, "Wu", E, F, d, sld, dev, seed)
+    else:
+        w["b1"] = (torch.rand((E, F), generator=_gen(dev, seed, wl, "b1"), device=dev) - 0.5) * 0.02
+        w["b2"] = (torch.rand((E, d), generator=_gen(dev, seed, wl, "b2"), device=dev) - 0.5) * 0.02
+    if S:
+        for name, rows, cols in (("Wsg", S, d), ("Wsd", d, S)) + ((("Wsu", S, d),) if wl.act == "swiglu" else ()):
+            c, sc = _fp8_block_stack(wl, name, 1, rows, cols, sld, dev, seed)
+            w[name], w[name + "_scale"] = c[0], sc[0]
+    return w

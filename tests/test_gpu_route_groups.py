@@ -1,0 +1,234 @@
+"""Group-limited routing against a 64-bit sort, row by row, and its gradient.
+
+Tolerances.  The choice is that of the 64-bit keys (block_reference.check_choice
+says what 64-bit arithmetic leaves open).  Gates
+and score sums: expf within 2 ulp on an argument that one subtraction rounded
+(|l - m| <= 32 here: 32 * 2^-24), a sum of at most 8 + 5 terms a warp, a
+reciprocal or quotient and three products: at most 2^-17.7 relative with the
+sum over 32 tokens; 2^-17 is used.  The gradient: the same relative error on
+each term that meets, twice (scores and normalisation): 2^-15 of the magnitudes.
+"""
+import pytest
+import torch
+
+from mixture_experts_layer_49_b200 import native as nat
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+TOL = 2.0 ** -17
+
+
+def config(T, E, k, score, renorm):
+    return nat.make_config(T, 8, E, 8, k, score=score, renorm=renorm)
+
+
+def run(logits, bias, k, groups, score="sigmoid", renorm=1):
+    T, E = logits.shape
+    cfg = config(T, E, k, score, renorm)
+    idx = torch.full((T + 1, k), -9, dtype=torch.int32, device=logits.device)
+    gate = torch.full((T + 1, k), -9.0, device=logits.device)
+    psum = torch.full(((T + 31) // 32 + 1, E), -9.0, device=logits.device)
+    nat.moe_route_select(cfg, nat.route_groups(*groups), logits, bias, idx, gate, psum)
+    assert (idx[T] == -9).all() and (gate[T] == -9).all() and (psum[-1] == -9).all()
+    return idx[:T], gate[:T], psum[:-1]
+
+
+def check(logits, bias, k, groups, score="sigmoid", renorm=1):
+    idx, gate, psum = run(logits, bias, k, groups, score, renorm)
+    l, b = logits.cpu(), None if bias is None else bias.cpu()
+    ref.check_choice(idx.cpu(), l, b, k, *groups[:3], score)
+    g = ref.gates(l, idx.cpu(), score, renorm, groups[3])
+    assert ((gate.cpu().double() - g).abs() <= g.abs() * TOL + 1e-37).all()
+    p = ref.score_sums(l, score)
+    assert ((psum.cpu().double() - p).abs() <= p.abs() * TOL + 1e-37).all()
+
+
+CASES = [
+    # E, k, groups
+    (256, 8, (8, 4, 2, 2.5)), (256, 8, (8, 4, 1, 1.0)), (256, 32, (4, 2, 2, 1.0)), (256, 1, (32, 1, 2, 1.0)),
+    (256, 6, (128, 5, 2, 1.0)), (256, 6, (256, 9, 1, 1.0)), (160, 6, (8, 3, 2, 16.0)), (128, 8, (4, 2, 2, 1.0)),
+    (128, 8, (1, 1, 1, 1.0)), (64, 4, (16, 3, 2, 1.0)), (60, 4, (5, 2, 2, 1.0)), (30, 5, (5, 3, 2, 1.0)),
+    (33, 3, (3, 2, 1, 1.0)), (32, 1, (8, 8, 2, 1.0)), (8, 2, (4, 2, 2, 1.0)), (7, 7, (1, 1, 2, 1.0)),
+    (250, 8, (25, 7, 2, 1.0)), (1, 1, (1, 1, 1, 2.0)),
+]
+
+
+@pytest.mark.parametrize("score,renorm,bias", [("sigmoid", 1, True), ("sigmoid", 0, False), ("softmax", 1, True),
+                                               ("softmax", 0, False)])
+@pytest.mark.parametrize("E,k,groups", CASES)
+def test_selection(cuda_device, E, k, groups, score, renorm, bias):
+    g = torch.Generator(device=cuda_device).manual_seed(E * 100 + k)
+    for T in (1, 45, 64):
+        logits = 2.0 * torch.randn((T, E), generator=g, device=cuda_device)
+        b = 0.3 * torch.randn(E, generator=g, device=cuda_device) if bias else None
+        check(logits, b, k, groups, score, renorm)
+
+
+def test_unaligned_rows(cuda_device):
+    g = torch.Generator(device=cuda_device).manual_seed(4)
+    raw = torch.randn(64 * 256 + 3, generator=g, device=cuda_device)
+    for off in (0, 1, 3):
+        logits = raw[off:off + 64 * 256].view(64, 256)
+        check(logits, None, 8, (8, 4, 2, 2.5))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_close_keys_are_told_apart(cuda_device, score):
+    """Logits a few units in the last place apart, and in saturated sigmoids: fp32
+    keys would tie or swap, the 64-bit values do not."""
+    T, E = 256, 64
+    g = torch.Generator(device=cuda_device).manual_seed(11)
+    base = torch.randn((T, 1), generator=g, device=cuda_device)
+    ulps = torch.randint(-6, 7, (T, E), generator=g, device=cuda_device)
+    logits = (base.view(torch.int32) + ulps.to(torch.int32)).view(torch.float32)
+    logits[64:128] = 12.0 + torch.randn((64, E), generator=g, device=cuda_device)        # sigmoids near 1
+    logits[128:160] = torch.randint(-3, 4, (32, E), generator=g, device=cuda_device).float()   # many exact ties
+    bias = 1e-7 * torch.randn(E, generator=g, device=cuda_device)
+    for b in (None, bias):
+        for groups in ((1, 1, 1, 1.0), (8, 3, 2, 1.0), (4, 2, 1, 1.0)):
+            check(logits.contiguous(), b, 6, groups, score)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_ties_take_the_lowest_ids(cuda_device, score):
+    idx, _, _ = run(torch.zeros((3, 32), device=cuda_device), None, 4, (4, 2, 2, 1.0), score)
+    assert (idx.cpu() == torch.arange(4, dtype=torch.int32)).all()
+    logits = torch.zeros((1, 32), device=cuda_device)
+    logits[0, ::2] = -0.0                                       # the same key
+    assert run(logits, None, 4, (4, 2, 2, 1.0), score)[0].tolist() == [[0, 1, 2, 3]]
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", 1), ("softmax", 1), ("softmax", 0)])
+def test_masked_and_non_finite_logits(cuda_device, score, renorm):
+    inf, nan = float("inf"), float("nan")
+    logits = torch.randn((40, 64), device=cuda_device, generator=torch.Generator(device=cuda_device).manual_seed(2))
+    logits[0] = -inf                                            # nothing left
+    logits[1, 3:] = -inf                                        # fewer experts left than are chosen
+    logits[2, 16:32] = -inf                                     # a whole group masked
+    logits[3] = torch.finfo(torch.float32).min
+    logits[4, ::2] = torch.finfo(torch.float32).min
+    logits[5, 17:] = -inf
+    groups = (8, 3, 2, 2.0)
+    check(logits, None, 4, groups, score, renorm)
+    idx, gate, psum = run(logits, None, 4, groups, score, renorm)
+    assert (gate[0] == 0).all() and idx[0].tolist() == [0, 1, 2, 3]
+    logits[6, 5] = nan
+    logits[7] = nan
+    logits[8, 9] = inf
+    logits[9, 8:16] = nan
+    idx2, gate2, _ = run(logits, None, 4, groups, score, renorm)
+    assert torch.equal(idx2[10:], idx[10:]) and torch.equal(gate2[10:], gate[10:])      # other rows as before
+    assert torch.equal(idx2[:6], idx[:6]) and torch.equal(gate2[:6], gate[:6])
+    assert torch.equal(idx2.cpu(), ref.select(logits.cpu(), None, 4, *groups[:3], score))
+    for row in idx2.tolist():
+        assert len(set(row)) == 4 and all(0 <= e < 64 for e in row)
+
+
+def test_extreme_bias_and_no_psum(cuda_device):
+    logits = torch.randn((70, 128), device=cuda_device)
+    bias = torch.zeros(128, device=cuda_device)
+    bias[7] = 1e30
+    bias[9] = -1e30
+    bias[40] = float("-inf")
+    for score in ("sigmoid", "softmax"):
+        check(logits, bias, 5, (4, 2, 2, 1.0), score)
+    cfg = config(70, 128, 5, "softmax", 1)
+    idx, gate = torch.empty((70, 5), dtype=torch.int32, device=cuda_device), torch.empty((70, 5), device=cuda_device)
+    nat.moe_route_select(cfg, nat.route_groups(4, 2), logits, bias, idx, gate)
+    assert torch.equal(idx.cpu(), ref.select(logits.cpu(), bias.cpu(), 5, 4, 2, 2, "softmax"))
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", 1), ("softmax", 1), ("softmax", 0)])
+@pytest.mark.parametrize("T,E,k,scale,alpha", [(1, 8, 1, 1.0, 0.0), (5, 256, 8, 2.5, 0.01), (70, 128, 8, 1.0, 1.0),
+                                               (33, 60, 4, 2.5, 0.5), (64, 33, 32, 1.0, 0.0), (9, 1, 1, 1.0, 1.0)])
+def test_gradient(cuda_device, T, E, k, scale, alpha, score, renorm):
+    g = torch.Generator(device=cuda_device).manual_seed(T + E)
+    logits = 2.0 * torch.randn((T, E), generator=g, device=cuda_device)
+    idx = ref.select(logits.cpu(), None, k, 1, 1, 1, score).to(cuda_device)
+    dgate = torch.randn((T, k), generator=g, device=cuda_device)
+    counts = torch.bincount(idx.flatten().long(), minlength=E).to(torch.int32)
+    cfg = config(T, E, k, score, renorm)
+    d = torch.full((T + 1, E), -9.0, device=cuda_device)
+    nat.moe_route_backward(cfg, nat.route_groups(1, 1, 1, scale), logits, idx, dgate, counts if alpha else None, alpha,
+                           d[:T])
+    assert (d[T] == -9).all()
+    args = (idx.cpu(), dgate.cpu(), counts.cpu(), alpha, score, renorm, scale)
+    want = ref.route_backward(logits.cpu(), *args)
+    s = ref.scores(logits.cpu(), score)
+    chosen = s.gather(1, idx.cpu().long())
+    total = chosen.sum(1, keepdim=True) if (score == "sigmoid" or renorm) else 1.0
+    # the magnitudes that meet: each score times the gradients it is weighed against
+    own = torch.zeros_like(s).scatter_add_(1, idx.cpu().long(), dgate.cpu().double().abs() * scale / total)
+    mean = (own * s).sum(1, keepdim=True)
+    bal = alpha * E / T * counts.cpu().double() / (T * k)
+    if score == "sigmoid":
+        z = s.sum(1, keepdim=True)
+        hit = torch.zeros_like(s).scatter_(1, idx.cpu().long(), 1.0)
+        size = s * (1 - s) * (own + hit * mean / total + (bal + (bal * s).sum(1, keepdim=True) / z) / z)
+    else:
+        size = s * (own + 2 * mean + bal + (bal * s).sum(1, keepdim=True))
+    assert ((d[:T].cpu().double() - want).abs() <= size * 2.0 ** -15 + 1e-37).all()
+
+
+def test_gradient_of_bad_and_masked_rows(cuda_device):
+    E, k = 64, 4
+    logits = torch.randn((6, E), device=cuda_device)
+    logits[1] = float("-inf")
+    logits[2, 8:] = float("-inf")
+    idx = torch.arange(k, dtype=torch.int32, device=cuda_device).repeat(6, 1).contiguous()
+    idx[3, 1] = -1
+    idx[4, 2] = E
+    dgate = torch.randn((6, k), device=cuda_device)
+    for score, renorm in (("sigmoid", 1), ("softmax", 1), ("softmax", 0)):
+        d = torch.empty((6, E), device=cuda_device)
+        nat.moe_route_backward(config(6, E, k, score, renorm), nat.route_groups(1, 1, 1), logits, idx, dgate, None, 0.0, d)
+        assert torch.isfinite(d).all() and (d[1] == 0).all() and (d[2, 8:] == 0).all()
+        ok = ref.route_backward(logits[:1].cpu(), idx[:1].cpu(), dgate[:1].cpu(), torch.zeros(E), 0.0, score, renorm, 1.0)
+        assert (d[0].cpu().double() - ok[0]).abs().max() < 1e-5
+
+
+def test_two_calls_in_a_graph(cuda_device):
+    T, E, k = 96, 256, 8
+    a, b = torch.randn((T, E), device=cuda_device), torch.randn((T, E), device=cuda_device)
+    cfg, groups = config(T, E, k, "sigmoid", 1), nat.route_groups(8, 4, 2, 2.5)
+    outs = [(torch.empty((T, k), dtype=torch.int32, device=cuda_device), torch.empty((T, k), device=cuda_device),
+             torch.empty((T // 32, E), device=cuda_device)) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for l, o in zip((a, b), outs):
+            nat.moe_route_select(cfg, groups, l, None, *o)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for l, o in zip((a, b), outs):
+        want = run(l, None, k, (8, 4, 2, 2.5))
+        assert all(torch.equal(x, y) for x, y in zip(o, want))
+
+
+def test_router_stage_agrees_with_the_selection_of_its_logits(cuda_device):
+    """moe_router_topk_groups on x: its logits_out selected again give its outputs."""
+    for dtype, T, d, E in (("bf16", 70, 256, 64), ("bf16", 1, 4096, 256), ("f32", 45, 128, 32)):
+        g = torch.Generator(device=cuda_device).manual_seed(d)
+        cfg = nat.make_config(T, d, E, 64, 4, dtype=dtype, score="sigmoid")
+        x = torch.randn((T, d), generator=g, device=cuda_device).to(nat.layer_dtype(cfg))
+        Wr = torch.randn((d, E), generator=g, device=cuda_device) / d ** 0.5
+        lb, sb = (0.1 * torch.randn(E, generator=g, device=cuda_device) for _ in range(2))
+        ws = nat.alloc_workspace(cfg)
+        idx, gate = torch.empty((T, 4), dtype=torch.int32, device=cuda_device), torch.empty((T, 4), device=cuda_device)
+        logits, psum = torch.empty((T, E), device=cuda_device), torch.empty((nat.router_blocks(cfg), E), device=cuda_device)
+        groups = nat.route_groups(8, 3, 2, 1.5)
+        nat.moe_router_topk_groups(cfg, groups, x, Wr, lb, sb, idx, gate, logits, psum, ws)
+        plain = [torch.empty_like(t) for t in (idx, gate, logits, psum)]
+        nat.moe_router_topk(cfg, x, Wr, lb, sb, *plain, ws)
+        assert torch.equal(plain[2], logits)
+        i2, g2, p2 = torch.empty_like(idx), torch.empty_like(gate), torch.empty_like(psum)
+        nat.moe_route_select(cfg, groups, logits, sb, i2, g2, p2)
+        assert torch.equal(i2, idx) and torch.equal(g2, gate) and torch.equal(p2, psum)
+        nat.moe_router_topk_groups(cfg, groups, x, Wr, lb, sb, i2, g2, None, p2, ws)     # no logits asked for
+        assert torch.equal(i2, idx) and torch.equal(g2, gate) and torch.equal(p2, psum)
+        # one group: the same experts as the plain router
+        nat.moe_router_topk_groups(cfg, nat.route_groups(1, 1, 1), x, Wr, lb, sb, i2, g2, None, p2, ws)
+        want = ref.select(logits.cpu(), sb.cpu(), 4, 1, 1, 1, "sigmoid")
+        assert torch.equal(i2.cpu(), want)
+        assert nat.moe_get_device_status(ws) == nat.MOE_OK
