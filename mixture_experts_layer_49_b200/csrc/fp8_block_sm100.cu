@@ -32,6 +32,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "sm100.cuh"
@@ -41,14 +43,15 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128, BN = 256, BK = 128;
-constexpr int STAGES = 4;
-constexpr int kThreads = 320;
+constexpr int STAGES = 3;
+constexpr int kThreads = 384;                // 3 warpgroups: control, 2 x sums
 constexpr uint32_t A_BYTES = BM * BK;
 constexpr uint32_t B_BYTES = BN * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kMaxGroups = 257;
-constexpr uint32_t kIdesc = make_idesc_e4m3(BM, BN);
+constexpr int BH = BN / 2;                          // columns of a unit: half a tile's
+constexpr uint32_t kIdesc = make_idesc_e4m3(BM, BH);
 
 enum { FB_SWIGLU = 0, FB_GELU = 1, FB_DOWN = 2 };
 
@@ -73,15 +76,18 @@ struct Params {
     int64_t ldo;
     float *out_scale;            // scale rows of the codes, ld_out_scale floats apart
     int64_t ld_out_scale;
+    int tail_mode;               // 1-CTA kernel: only last blocks of 1..128 rows
     uint64_t timeout_ns;
 };
 
-struct Tail {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
-    uint64_t accf[2];
-    uint64_t acce[2];
-    uint64_t drain;
+// Barriers and the tile table behind the stages; NS stages.
+template <int NS>
+struct TailT {
+    uint64_t full[NS];
+    uint64_t empty[NS];
+    uint64_t accf[4];            // unit 2 * half + (K block & 1)
+    uint64_t acce[4];
+    uint64_t drain[2];
     uint64_t xch[4];             // SwiGLU: both halves of a quadrant's rows left their maxima
     uint32_t tmem_base;
     int abort_flag;
@@ -89,46 +95,48 @@ struct Tail {
     int mtiles[kMaxGroups];
     int rows[kMaxGroups];
     int row0[kMaxGroups];
+    int start[kMaxGroups];       // first row of the group that this launch computes
     float amax[2][2][BM];        // SwiGLU: the two halves' row maxima, two tiles deep
 };
-constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + sizeof(Tail);
+using Tail = TailT<STAGES>;
+// Output staging: 32 rows of 256 bytes per sums warp.
+constexpr uint32_t STG_BYTES = 32 * 256;
+constexpr size_t kStgOff = (STAGES * STAGE_BYTES + sizeof(Tail) + 1023) / 1024 * 1024;
+constexpr size_t kSmemBytes = 1024 + kStgOff + 8 * STG_BYTES;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * (1.f + erff(v * 0.70710678118654752f)); }
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
+// One lane of the converged warp, always the same one.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A bounded wait of the whole warp with one verdict for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t addr, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(addr, parity, limit_ns));
+}
+
+template <class Tail>
 __device__ __forceinline__ bool aborted(const Tail &s) {
     return *reinterpret_cast<const volatile int *>(&s.abort_flag) != 0;
 }
+template <class Tail>
 __device__ __forceinline__ void fail(Tail &s, const Params &p, int where) {
     record_error(p.status, MOE_ERR_TIMEOUT, where);
     *reinterpret_cast<volatile int *>(&s.abort_flag) = 1;
 }
 
-__device__ __forceinline__ void decode(const Tail &s, int G, int tile, int &g, int &mt, int &nt) {
-    int lo = 0, hi = G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s.tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    g = lo;
-    const int local = tile - s.tile_start[g];
-    mt = local % s.mtiles[g];
-    nt = local / s.mtiles[g];
-}
-
-// Two fp32 fused multiply-adds in one instruction: (a0, a1) += (v0, v1) * s.
-__device__ __forceinline__ void fma2(float &a0, float &a1, float v0, float v1, uint64_t s) {
-    uint64_t a, v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(s));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
-}
-__device__ __forceinline__ uint64_t both(float s) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(s));
-    return d;
+// The group of tile `tile`, from the group of an earlier one; mt runs fastest
+// within a group, so CTAs at work together share weight tiles through L2.
+template <class Tail>
+__device__ __forceinline__ void locate(const Tail &s, int tile, int &g, int &mt, int &nt) {
+    while (s.tile_start[g + 1] <= tile) ++g;
+    const int local = tile - s.tile_start[g], n = s.mtiles[g];
+    nt = local / n;
+    mt = local - nt * n;
 }
 
 // Codes of 16 values v * inv as one 16-byte vector.
@@ -143,6 +151,38 @@ __device__ __forceinline__ uint4 codes16(const float *v, float inv) {
         w[h] = (uint32_t)lo | ((uint32_t)hi << 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The warp's 32 rows of P 16-byte pieces through its staging buffer: each lane
+// writes its row, then neighbouring lanes store neighbouring pieces (stores by
+// row would touch 32 rows per instruction: 4096 more cycles a tile measured;
+// TMA stores need a proxy fence, which waits 500 to 3000 cycles beside the
+// loads).  Piece p of row r lies at an XOR of p, so both sides are free of bank
+// conflicts.
+template <int P>
+__device__ __forceinline__ uint32_t piece_addr(uint32_t stg, int r, int p) {
+    const int x = P == 4 ? (p ^ ((r >> 1) & 3)) : (p ^ (r & 7));
+    return stg + r * (P * 16) + (x << 4);
+}
+template <int P>
+__device__ __forceinline__ void stage_put(uint32_t stg, int p, uint4 w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece_addr<P>(stg, threadIdx.x & 31, p)), "r"(w.x),
+                 "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+// rows: valid rows of the warp; pieces: those below the row's end.
+template <int P>
+__device__ __forceinline__ void stage_out(uint32_t stg, char *out, int64_t ld, int rows, int pieces) {
+    const int lane = threadIdx.x & 31, p = lane % P;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int r = i * (32 / P) + lane / P;
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(piece_addr<P>(stg, r, p)) : "memory");
+        if (r < rows && p < pieces) *reinterpret_cast<uint4 *>(out + r * ld + p * 16) = w;
+    }
+    __syncwarp();
 }
 
 // What one sums thread knows of its tile: its output row and scale sources.
@@ -186,26 +226,25 @@ __device__ __forceinline__ RowCtx row_ctx(const Params &p, bool sh, int e, int n
 // false: a wait ran out.
 template <int MODE>
 __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, float (&acc)[128], float (*amax_buf)[BM],
-                                           int r_in_tile, uint32_t xch, uint32_t xphase) {
+                                           int r_in_tile, uint32_t xch, uint32_t xphase, uint32_t stg) {
+    const int rows = __popc(__ballot_sync(0xffffffffu, c.valid));     // a prefix of the warp's lanes
+    const int64_t row0 = c.orow - (int)(threadIdx.x & 31);
     if (MODE == FB_DOWN) {
         const int col0 = c.nt * BN + c.half * 128;
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + c.orow * p.ldo + col0;
+        if (c.bias) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] += col0 + i < c.N ? __ldg(c.bias + col0 + i) : 0.f;
+        }
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
-            if (!c.valid || col0 + u * 8 >= c.N) continue;
-            uint4 pk;
-            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&pk);
+            uint4 w;
+            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float a = acc[u * 8 + 2 * i], b = acc[u * 8 + 2 * i + 1];
-                if (c.bias) {
-                    a += __ldg(c.bias + col0 + u * 8 + 2 * i);
-                    b += __ldg(c.bias + col0 + u * 8 + 2 * i + 1);
-                }
-                h[i] = __floats2bfloat162_rn(a * c.gate, b * c.gate);
-            }
-            *reinterpret_cast<uint4 *>(o + u * 8) = pk;
+            for (int i = 0; i < 4; ++i)
+                h[i] = __floats2bfloat162_rn(acc[u * 8 + 2 * i] * c.gate, acc[u * 8 + 2 * i + 1] * c.gate);
+            stage_put<16>(stg, u, w);
         }
+        stage_out<16>(stg, static_cast<char *>(p.out) + (row0 * p.ldo + col0) * 2, p.ldo * 2, rows, (c.N - col0) / 8);
         return true;
     }
     constexpr int W = MODE == FB_SWIGLU ? 64 : 128;        // hidden values of this thread
@@ -229,59 +268,37 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
         amax = fmaxf(amax, amax_buf[c.half ^ 1][r_in_tile]);
     } else {
+        if (c.bias) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] += col0 + i < c.N ? __ldg(c.bias + col0 + i) : 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < 128; ++i) {
-            const float b = (c.bias && col0 + i < c.N) ? __ldg(c.bias + col0 + i) : 0.f;
-            acc[i] = gelu_erf(acc[i] + b);                 // columns past N: gelu(0) = 0
+            acc[i] = gelu_erf(acc[i]);                     // columns past N: gelu(0) = 0
             amax = fmaxf(amax, fabsf(acc[i]));
         }
     }
     amax = fmaxf(amax, 0x1p-100f);
-    if (!c.valid) return true;
     const float inv = __fdiv_rn(448.f, amax);
-    uint8_t *o = static_cast<uint8_t *>(p.out) + c.orow * p.ldo + col0;
 #pragma unroll
-    for (int u = 0; u < W / 16; ++u)
-        if (col0 + u * 16 < c.N) *reinterpret_cast<uint4 *>(o + u * 16) = codes16(acc + u * 16, inv);
+    for (int u = 0; u < W / 16; ++u) stage_put<W / 16>(stg, u, codes16(acc + u * 16, inv));
+    stage_out<W / 16>(stg, static_cast<char *>(p.out) + row0 * p.ldo + col0, p.ldo, rows, (c.N - col0) / 16);
+    if (!c.valid) return true;
     const int blk = MODE == FB_SWIGLU ? c.nt : c.nt * 2 + c.half;
     if ((MODE != FB_SWIGLU || c.half == 0) && blk * 128 < c.N)
         p.out_scale[c.orow * p.ld_out_scale + blk] = __fdiv_rn(amax, 448.f);
     return true;
 }
 
-template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
-fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
-               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
-               const __grid_constant__ CUtensorMap tmBs, const __grid_constant__ CUtensorMap tmBs2,
-               const __grid_constant__ Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_addr = smem_u32(smem_raw);
-    const uint32_t base = (raw_addr + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (base - raw_addr);
-    Tail &s = *reinterpret_cast<Tail *>(smem + STAGES * STAGE_BYTES);
-    const uint32_t smA = base;
-    const uint32_t smB = base + STAGES * A_BYTES;
-
+// The tile list of a launch from the device-side offsets: groups are the routed
+// experts and, last, the shared expert.  TILES_PAIR: 256-row blocks and a last
+// block of more than 128 rows; TILES_TAIL: a last block of 1..128 rows, the rest
+// of the same groups; TILES_ALL: 128-row blocks of everything.
+enum { TILES_ALL = 0, TILES_TAIL = 1, TILES_PAIR = 2 };
+template <int BNO, class Tail>
+__device__ __forceinline__ void build_tiles(Tail &s, const Params &p, int which) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int BNO = MODE == FB_SWIGLU ? 128 : 256;     // output columns per tile
     const int G = p.E + (p.has_shared ? 1 : 0);
-
-    if (tid == 0) {
-        s.abort_flag = 0;
-        for (int i = 0; i < STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 8); }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.xch[i]), 2);
-        mbar_init(smem_u32(&s.drain), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    if (warp == 1) tmem_alloc(smem_u32(&s.tmem_base), TMEM_COLS);
-    if (tid == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
-    }
-    pdl_wait_then_release();
     if (tid == 0) s.tile_start[0] = 0;
     for (int g = tid; g < G; g += kThreads) {
         const bool sh = g >= p.E;
@@ -291,10 +308,18 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             record_error(p.status, MOE_ERR_DEVICE_BOUNDS, g);
             r0 = rows = 0;
         }
+        int start = 0, mt = (int)((rows + BM - 1) / BM);
+        const int rem = (int)(rows % (2 * BM));
+        if (which == TILES_TAIL) {
+            start = (int)rows - rem;
+            mt = (rem > 0 && rem <= BM) ? 1 : 0;
+        } else if (which == TILES_PAIR) {
+            mt = (int)(rows / (2 * BM)) + (rem > BM ? 1 : 0);
+        }
         const int n = sh ? p.N_shared : p.N_routed;
-        const int mt = (int)((rows + BM - 1) / BM);
         s.rows[g] = (int)rows;
         s.row0[g] = (int)r0;
+        s.start[g] = start;
         s.mtiles[g] = mt > 0 ? mt : 1;
         s.tile_start[g + 1] = mt * ((n + BNO - 1) / BNO);
     }
@@ -313,23 +338,130 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             carry += __shfl_sync(0xffffffffu, v, 31);
         }
     }
+}
+
+// The work of warps 4..11: two per TMEM lane quadrant, each half of the
+// columns.  PAIR: the CTA's rows are the rank-th 128 of a 256-row tile and the
+// accumulators are freed at the first CTA's barriers.
+template <int MODE, bool PAIR, class Tail>
+__device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tmem_base, uint32_t stg0, int total,
+                                           int tile0, int step, int rank) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int r_in_tile = q * 32 + lane;
+    const uint32_t stg = stg0 + (uint32_t)(warp - 4) * STG_BYTES;
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
+    constexpr int TM = PAIR ? 2 * BM : BM;
+    uint32_t cnt = 0;
+    uint32_t flip = 0;                                     // parity of the tiles this CTA has done
+    bool ok = true;
+    int g = 0;
+    for (int tile = tile0; tile < total && ok; tile += step, flip ^= 1u) {
+        int mt, nt;
+        locate(s, tile, g, mt, nt);
+        const bool sh = g >= p.E;
+        const int grow = s.start[g] + mt * TM + rank * BM + r_in_tile;
+        const int64_t first = sh ? 0 : (int64_t)s.row0[g];
+        const int64_t a_off = sh ? p.shared_a_row : 0, o_off = sh ? p.shared_out_row : 0;
+        const RowCtx c = row_ctx<MODE>(p, sh, g, nt, half, a_off + first + grow, a_off + first,
+                                       o_off + first + grow, grow < s.rows[g]);
+        const int nk = ((sh ? p.K_shared : p.K_routed) + BK - 1) / BK;
+        float acc[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        float ra = __ldg(c.sa), rw0 = __ldg(c.sw0), rw1 = __ldg(c.sw1);
+        for (int kb = 0; kb < nk; ++kb, ++cnt) {
+            const uint32_t unit = (uint32_t)half * 2 + (cnt & 1u), aphase = (cnt >> 1) & 1u;
+            const float s0 = ra * rw0, s1 = ra * rw1;
+            if (kb + 1 < nk) {                             // the next block's scales arrive during this one
+                ra = __ldg(c.sa + kb + 1);
+                rw0 = __ldg(c.sw0 + kb + 1);
+                rw1 = MODE == FB_SWIGLU ? __ldg(c.sw1 + kb + 1) : rw0;
+            }
+            if (!warp_wait(smem_u32(&s.accf[unit]), aphase, p.timeout_ns)) { if (lane == 0) fail(s, p, 64); ok = false; break; }
+            tc_fence_after();
+            const uint32_t ta = lane_addr + unit * BH;     // SwiGLU: 64 gate, then 64 up columns
+            float v[64];
+            tmem_ld32x2(ta, ta + 32, v);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = fmaf(v[i], s0, acc[i]);
+            tmem_ld32x2(ta + 64, ta + 96, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {                               // the accumulator is free: its words are in registers
+                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[unit]), 0));
+                else mbar_arrive(smem_u32(&s.acce[unit]));
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[64 + i] = fmaf(v[i], s1, acc[64 + i]);
+        }
+        if (!ok) break;
+        ok = finish_row<MODE>(p, c, acc, s.amax[flip], r_in_tile, smem_u32(&s.xch[q]), flip, stg);
+        if (!ok && lane == 0) fail(s, p, 67);
+    }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
+               const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
+               const __grid_constant__ CUtensorMap tmBs, const __grid_constant__ CUtensorMap tmBs2,
+               const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_addr);
+    Tail &s = *reinterpret_cast<Tail *>(smem + STAGES * STAGE_BYTES);
+    const uint32_t smA = base;
+    const uint32_t smB = base + STAGES * A_BYTES;
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);        // uniform for the compiler too
+    constexpr int BNO = MODE == FB_SWIGLU ? 128 : 256;     // output columns per tile
+    if (tid == 0) {
+        s.abort_flag = 0;
+        for (int i = 0; i < STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 2); }
+        for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 4); }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.xch[i]), 2);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&s.tmem_base), TMEM_COLS);
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
+    }
+    // Last blocks (tail mode) touch only rows the CTA-pair launch before them
+    // leaves alone and read only what the kernel before that wrote (complete
+    // once the pair launch started, which is when this launch can begin), so
+    // they start at once on the SMs the pair launch frees and wait for it only
+    // before exiting: whatever waits for this launch then sees both results.
+    if (p.tail_mode) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    else pdl_wait_then_release();
+    build_tiles<BNO>(s, p, p.tail_mode ? TILES_TAIL : TILES_ALL);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int total = s.tile_start[G];
+    const int total = s.tile_start[p.E + (p.has_shared ? 1 : 0)];
     const uint32_t tmem_base = s.tmem_base;
 
-    if (warp == 0) {
+    // registers: launched with 168 a thread (3 x 128 x 168), redistributed as
+    // 128 x 88 + 256 x 208, the same total
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp == 0) {
         // ================= TMA producer
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0, issued = 0;
+            int g = 0;
             for (int tile = blockIdx.x; tile < total && !aborted(s); tile += gridDim.x) {
-                int g, mt, nt;
-                decode(s, G, tile, g, mt, nt);
+                int mt, nt;
+                locate(s, tile, g, mt, nt);
                 const bool sh = g >= p.E;
                 const int nk = ((sh ? p.K_shared : p.K_routed) + BK - 1) / BK;
-                const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + mt * BM;
+                const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + s.start[g] + mt * BM;
                 const CUtensorMap *mA = sh ? &tmAs : &tmA;
                 const CUtensorMap *mB = sh ? &tmBs : &tmB;
                 const CUtensorMap *mB2 = sh ? &tmBs2 : &tmB2;
@@ -339,12 +471,10 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     const uint32_t fb = smem_u32(&s.full[stage]);
                     mbar_arrive_expect_tx(fb, STAGE_BYTES);
                     tma_load_2d(smA + stage * A_BYTES, mA, fb, kb * BK, a_row);
-                    if (MODE == FB_SWIGLU) {
-                        tma_load_3d(smB + stage * B_BYTES, mB, fb, kb * BK, nt * 128, e);
-                        tma_load_3d(smB + stage * B_BYTES + B_BYTES / 2, mB2, fb, kb * BK, nt * 128, e);
-                    } else {
-                        tma_load_3d(smB + stage * B_BYTES, mB, fb, kb * BK, nt * BN, e);
-                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)            // unit u / 2, its first or second 64 columns
+                        tma_load_3d(smB + stage * B_BYTES + u * (B_BYTES / 4), MODE == FB_SWIGLU && (u & 1) ? mB2 : mB, fb,
+                                    kb * BK, MODE == FB_SWIGLU ? nt * 128 + (u >> 1) * 64 : nt * BN + u * 64, e);
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -353,96 +483,47 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
                 if (!mbar_wait(smem_u32(&s.full[i % STAGES]), (i / STAGES) & 1u, p.timeout_ns)) fail(s, p, 65);
         }
-    } else if (warp == 1) {
-        // ================= MMA issuer: one accumulator per K block
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, cnt = 0;
-            for (int tile = blockIdx.x; tile < total && !aborted(s); tile += gridDim.x) {
-                // the shared group, when there is one, is the last
-                const int nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
-                bool ok = true;
-                for (int kb = 0; kb < nk; ++kb, ++cnt) {
-                    const uint32_t ab = cnt & 1u, aphase = (cnt >> 1) & 1u;
-                    if (!mbar_wait(smem_u32(&s.acce[ab]), aphase ^ 1u, p.timeout_ns)) { fail(s, p, 62); ok = false; break; }
-                    if (!mbar_wait(smem_u32(&s.full[stage]), phase, p.timeout_ns)) { fail(s, p, 63); ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a0 = smA + stage * A_BYTES, b0 = smB + stage * B_BYTES;
-#pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        mma_e4m3(tmem_base + ab * BN, sdesc(a0 + k * 32), sdesc(b0 + k * 32), kIdesc, k ? 1u : 0u);
-                    mma_commit(smem_u32(&s.empty[stage]));
-                    mma_commit(smem_u32(&s.accf[ab]));
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                }
-                if (!ok) break;
-            }
-            if (aborted(s)) {                              // products in flight end before TMEM is freed
-                mma_commit(smem_u32(&s.drain));
-                if (!mbar_wait(smem_u32(&s.drain), 0, p.timeout_ns)) fail(s, p, 66);
-            }
-        }
-    } else {
-        // ================= scaled sums and epilogue: warps 2..9
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        const int r_in_tile = q * 32 + lane;
-        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
-        // columns of this warp: SwiGLU 64 gate and 64 up columns, else 128 in a row
-        const uint32_t c0 = MODE == FB_SWIGLU ? half * 64 : half * 128;
-        const uint32_t c1 = MODE == FB_SWIGLU ? 128 + half * 64 : half * 128 + 64;
-        uint32_t cnt = 0;
-        uint32_t flip = 0;                                 // parity of the tiles this CTA has done
+      } else if (warp < 3) {
+        // ================= MMA issuers: warp 1 the first unit of every K block,
+        // warp 2 the second, each alternating between two accumulators.  The
+        // whole warp runs the loop, so that descriptors stay in uniform
+        // registers; one lane issues (with a single-lane loop the issue took
+        // 500 cycles per K block beside the busy sums warps).
+        const uint32_t half = warp - 1;
+        const bool leader = elect_lane();
+        const uint64_t da0 = sdesc(smA), db0 = sdesc(smB + half * (B_BYTES / 2));
+        uint32_t i = 0;                                    // K blocks done
         bool ok = true;
-        for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, flip ^= 1u) {
-            int g, mt, nt;
-            decode(s, G, tile, g, mt, nt);
-            const bool sh = g >= p.E;
-            const int grow = mt * BM + r_in_tile;
-            const int64_t first = sh ? 0 : (int64_t)s.row0[g];
-            const int64_t a_off = sh ? p.shared_a_row : 0, o_off = sh ? p.shared_out_row : 0;
-            const RowCtx c = row_ctx<MODE>(p, sh, g, nt, half, a_off + first + grow, a_off + first,
-                                           o_off + first + grow, grow < s.rows[g]);
-            const int nk = ((sh ? p.K_shared : p.K_routed) + BK - 1) / BK;
-            float acc[128];
-#pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-            float ra = __ldg(c.sa), rw0 = __ldg(c.sw0), rw1 = __ldg(c.sw1);
-            for (int kb = 0; kb < nk; ++kb, ++cnt) {
-                const uint32_t ab = cnt & 1u, aphase = (cnt >> 1) & 1u;
-                const uint64_t s0 = both(ra * rw0), s1 = both(ra * rw1);
-                if (kb + 1 < nk) {                         // the next block's scales arrive during this one
-                    ra = __ldg(c.sa + kb + 1);
-                    rw0 = __ldg(c.sw0 + kb + 1);
-                    rw1 = MODE == FB_SWIGLU ? __ldg(c.sw1 + kb + 1) : rw0;
-                }
-                // lane 0 waits, the warp follows its verdict
-                int okw = 1;
-                if (lane == 0) okw = (!aborted(s) && mbar_wait(smem_u32(&s.accf[ab]), aphase, p.timeout_ns)) ? 1 : 0;
-                okw = __shfl_sync(0xffffffffu, okw, 0);
-                if (!okw) { if (lane == 0) fail(s, p, 64); ok = false; break; }
+        for (int tile = blockIdx.x; tile < total && ok && !aborted(s); tile += gridDim.x) {
+            // the shared group, when there is one, is the last
+            const int nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
+            for (int kb = 0; kb < nk; ++kb, ++i) {
+                const uint32_t stage = i % STAGES, phase = (i / STAGES) & 1u, aphase = (i >> 1) & 1u;
+                const uint32_t unit = half * 2 + (i & 1u);
+                if (!warp_wait(smem_u32(&s.acce[unit]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 62); ok = false; break; }
+                if (!warp_wait(smem_u32(&s.full[stage]), phase, p.timeout_ns)) { if (leader) fail(s, p, 63); ok = false; break; }
                 tc_fence_after();
-                const uint32_t ta = lane_addr + ab * BN;
+                const uint64_t da = da0 + stage * (A_BYTES >> 4), db = db0 + stage * (B_BYTES >> 4);
+                const uint32_t dtm = tmem_base + unit * BH;
+                if (leader) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t tc = ta + (h ? c1 : c0);
-                    const uint64_t sc = h ? s1 : s0;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float v[32];
-                        tmem_ld32(tc + u * 32, v);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            fma2(acc[h * 64 + u * 32 + i], acc[h * 64 + u * 32 + i + 1], v[i], v[i + 1], sc);
-                    }
+                    for (int k = 0; k < BK / 32; ++k) mma_e4m3(dtm, da + k * 2, db + k * 2, kIdesc, k ? 1u : 0u);
+                    mma_commit(smem_u32(&s.accf[unit]));
+                    mma_commit(smem_u32(&s.empty[stage]));
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&s.acce[ab]));
             }
-            if (!ok) break;
-            ok = finish_row<MODE>(p, c, acc, s.amax[flip], r_in_tile, smem_u32(&s.xch[q]), flip);
-            if (!ok && lane == 0) fail(s, p, 67);
         }
+        if (aborted(s) && leader) {                        // products in flight end before TMEM is freed
+            mma_commit(smem_u32(&s.drain[half]));
+            if (!mbar_wait(smem_u32(&s.drain[half]), 0, p.timeout_ns)) fail(s, p, 66);
+        }
+        __syncwarp();
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ================= scaled sums and epilogue: warps 4..11
+        sums_warps<MODE, false>(s, p, tmem_base, base + (uint32_t)kStgOff, total, blockIdx.x, gridDim.x, 0);
     }
 
     tc_fence_before();
@@ -452,16 +533,212 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
     }
+    if (p.tail_mode) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ============================================================================
+// CTA pairs: a cluster of two computes 256 rows x 256 accumulator columns with
+// tcgen05.mma.cta_group::2.  Each CTA loads its own 128 A rows and half of the B
+// rows (SwiGLU: gate rows in the first CTA, up rows in the second), so a K block
+// moves 32 KiB per CTA through L2 instead of 48; at 48 KiB the L2 limits the
+// 1-CTA kernel to about 850 cycles a block.  The first CTA issues the products;
+// its full barriers collect both CTAs' copies, its commits reach both CTAs'
+// empty and accumulator-full barriers, and both CTAs' sums warps free the
+// accumulators at its barriers.
+constexpr int P_STAGES = 4;
+constexpr uint32_t P_STAGE_BYTES = A_BYTES + B_BYTES / 2;
+constexpr uint32_t kIdescPair = make_idesc_e4m3(2 * BM, BH);
+using PairTail = TailT<P_STAGES>;
+constexpr size_t kPairStgOff = (P_STAGES * P_STAGE_BYTES + sizeof(PairTail) + 1023) / 1024 * 1024;
+constexpr size_t kPairSmemBytes = 1024 + kPairStgOff + 8 * STG_BYTES;
+static_assert(kPairSmemBytes <= 227 * 1024, "pair kernel shared memory");
+
 template <int MODE>
-cudaError_t launch_gemm(const CUtensorMap &A, const CUtensorMap &As, const CUtensorMap &B, const CUtensorMap &B2,
-                        const CUtensorMap &Bs, const CUtensorMap &Bs2, const Params &p, int grid, cudaStream_t st,
-                        bool pdl) {
-    cudaError_t e = cudaFuncSetAttribute(fp8_block_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
+                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
+                    const __grid_constant__ CUtensorMap tmBs, const __grid_constant__ CUtensorMap tmBs2,
+                    const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_addr);
+    PairTail &s = *reinterpret_cast<PairTail *>(smem + P_STAGES * P_STAGE_BYTES);
+    const uint32_t smA = base;
+    const uint32_t smB = base + P_STAGES * A_BYTES;
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const uint32_t rank = cluster_ctarank();
+    const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
+    constexpr int BNO = MODE == FB_SWIGLU ? 128 : 256;
+
+    if (tid == 0) {
+        s.abort_flag = 0;
+        for (int i = 0; i < P_STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 2); }
+        for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 8); }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.xch[i]), 2);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&s.tmem_base), TMEM_COLS);   // warp 1 of both CTAs
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB2) : "memory");
+    }
+    pdl_wait_then_release();
+    build_tiles<BNO>(s, p, TILES_PAIR);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                        // both CTAs' barriers are initialised
+    tc_fence_after();
+    const int total = s.tile_start[p.E + (p.has_shared ? 1 : 0)];
+    const uint32_t tmem_base = s.tmem_base;
+
+    // registers as in the 1-CTA kernel
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp == 0) {
+        // ================= TMA producer (both CTAs)
+        if (lane == 0) {
+            uint32_t i = 0;                                // K blocks loaded
+            int g = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok && !aborted(s); tile += npairs) {
+                int mt, nt;
+                locate(s, tile, g, mt, nt);
+                const bool sh = g >= p.E;
+                const int nk = ((sh ? p.K_shared : p.K_routed) + BK - 1) / BK;
+                const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + mt * 2 * BM + (int)rank * BM;
+                const CUtensorMap *mA = sh ? &tmAs : &tmA;
+                const CUtensorMap *mB = (MODE == FB_SWIGLU && rank == 1) ? (sh ? &tmBs2 : &tmB2) : (sh ? &tmBs : &tmB);
+                // this CTA's 64 rows of each unit's 128 (SwiGLU: gate or up)
+                const int b_row = MODE == FB_SWIGLU ? nt * 128 : nt * BN + (int)rank * 64;
+                constexpr int kUnitRows = MODE == FB_SWIGLU ? 64 : 128;
+                const int e = sh ? 0 : g;
+                for (int kb = 0; kb < nk; ++kb, ++i) {
+                    const uint32_t stage = i % P_STAGES, phase = (i / P_STAGES) & 1u;
+                    if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.timeout_ns)) { fail(s, p, 71); ok = false; break; }
+                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), 2 * P_STAGE_BYTES);
+                    tma_load_2d_pair(smA + stage * A_BYTES, mA, fb, kb * BK, a_row);
+                    tma_load_3d_pair(smB + stage * (B_BYTES / 2), mB, fb, kb * BK, b_row, e);
+                    tma_load_3d_pair(smB + stage * (B_BYTES / 2) + B_BYTES / 4, mB, fb, kb * BK, b_row + kUnitRows, e);
+                }
+            }
+            // every copy has landed before the pair may end: the last use of each stage
+            if (rank == 0)
+                for (uint32_t j = i > P_STAGES ? i - P_STAGES : 0; j < i; ++j)
+                    if (!mbar_wait(smem_u32(&s.full[j % P_STAGES]), (j / P_STAGES) & 1u, p.timeout_ns)) fail(s, p, 75);
+        }
+      } else if (warp < 3) {
+        // ================= MMA issuers (first CTA): first and second units
+        if (rank == 0) {
+            const uint32_t half = warp - 1;
+            const bool leader = elect_lane();
+            const uint64_t da0 = sdesc(smA), db0 = sdesc(smB + half * (B_BYTES / 4));
+            uint32_t i = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok && !aborted(s); tile += npairs) {
+                const int nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
+                for (int kb = 0; kb < nk; ++kb, ++i) {
+                    const uint32_t stage = i % P_STAGES, phase = (i / P_STAGES) & 1u, aphase = (i >> 1) & 1u;
+                    const uint32_t unit = half * 2 + (i & 1u);
+                    if (!warp_wait(smem_u32(&s.acce[unit]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 72); ok = false; break; }
+                    if (!warp_wait(smem_u32(&s.full[stage]), phase, p.timeout_ns)) { if (leader) fail(s, p, 73); ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t da = da0 + stage * (A_BYTES >> 4), db = db0 + stage * (B_BYTES >> 5);
+                    const uint32_t dtm = tmem_base + unit * BH;
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < BK / 32; ++k) mma_e4m3_pair(dtm, da + k * 2, db + k * 2, kIdescPair, k ? 1u : 0u);
+                        mma_commit_pair(smem_u32(&s.accf[unit]), (uint16_t)0x3);
+                        mma_commit_pair(smem_u32(&s.empty[stage]), (uint16_t)0x3);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (aborted(s) && leader) {                    // products in flight end before TMEM is freed
+                mma_commit_pair(smem_u32(&s.drain[half]), (uint16_t)0x1);
+                if (!mbar_wait(smem_u32(&s.drain[half]), 0, p.timeout_ns)) fail(s, p, 76);
+            }
+            __syncwarp();
+        }
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        sums_warps<MODE, true>(s, p, tmem_base, base + (uint32_t)kPairStgOff, total, pair, npairs, (int)rank);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                        // no CTA leaves while its peer may still signal it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+// CTAs of a launch of `kernel` on the current device, found once per device
+// (0: not yet); pair: as many clusters of two as fit at a time.
+template <typename K>
+cudaError_t grid_of(std::atomic<int> (&cache)[64], K kernel, size_t smem, int num_sms, bool pair, int *grid) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return launch_kernel(fp8_block_gemm<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, pdl, A, As, B, B2, Bs, Bs2, p);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    *grid = cache[dev].load(std::memory_order_relaxed);
+    if (*grid) return cudaSuccess;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    int n = num_sms;
+    if (pair) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        n *= 2;
+    }
+    cache[dev].store(n, std::memory_order_relaxed);
+    *grid = n;
+    return cudaSuccess;
+}
+
+// Tensor maps of one product: A and weights.
+struct Maps {
+    CUtensorMap A, As, B, B2, Bs, Bs2;
+};
+
+// One product.  Without groups of more than 128 rows (few: no group can have
+// more) one launch of 128-row tiles; else the pair launch and, overlapping it,
+// the last blocks of 1..128 rows.
+template <int MODE>
+cudaError_t launch_product(const Maps &m, Params p, bool few, int num_sms, cudaStream_t st, bool pdl) {
+    static std::atomic<int> one[64], two[64];
+    int grid = 0;
+    cudaError_t e;
+    p.tail_mode = few ? 0 : 1;
+    if (!few) {
+        if ((e = grid_of(two, fp8_block_gemm_pair<MODE>, kPairSmemBytes, num_sms, true, &grid)) != cudaSuccess) return e;
+        e = launch_kernel(fp8_block_gemm_pair<MODE>, dim3(grid), dim3(kThreads), kPairSmemBytes, st, pdl, m.A, m.As, m.B,
+                          m.B2, m.Bs, m.Bs2, p);
+        if (e != cudaSuccess) return e;
+        pdl = true;
+    }
+    if ((e = grid_of(one, fp8_block_gemm<MODE>, kSmemBytes, num_sms, false, &grid)) != cudaSuccess) return e;
+    return launch_kernel(fp8_block_gemm<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, pdl, m.A, m.As, m.B, m.B2, m.Bs,
+                         m.Bs2, p);
 }
 
 }  // namespace
@@ -473,20 +750,23 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     const uint64_t routed = a.routed_rows > 0 ? (uint64_t)a.routed_rows : 1;
     const uint64_t all = (uint64_t)(a.shared_base + (has_sh ? a.T : 0));
     const uint64_t d = a.d, F = a.F, S = a.S;
-    const uint32_t box1 = swiglu ? 128 : BN;
-    CUtensorMap A1, A1s, B1, B1u, B1s, B1su, A2, A2s, B2, B2s;
-    bool ok = make_map(&A1, 2, a.x_perm, d, routed, 1, d, 0, BM, 1) &&
-              make_map(&B1, 3, a.W1, d, F, a.E, d, F * d, box1, 1) &&
-              make_map(&A2, 2, a.H8, F, all, 1, a.hF, 0, BM, 1) &&
-              make_map(&B2, 3, a.W2, F, d, a.E, F, d * F, BN, 1);
-    B1u = B1;
-    if (ok && swiglu) ok = make_map(&B1u, 3, a.Wu, d, F, a.E, d, F * d, box1, 1);
-    A1s = A1; B1s = B1; B1su = B1u; A2s = A2; B2s = B2;
+    // weight boxes of 64 rows: half a unit, or a pair CTA's share of one
+    auto weights = [](CUtensorMap *m, const uint8_t *w, uint64_t in, uint64_t out, uint64_t n) {
+        return make_map(m, 3, w, in, out, n, in, out * in, 64, 1);
+    };
+    Maps m1, m2;
+    bool ok = make_map(&m1.A, 2, a.x_perm, d, routed, 1, d, 0, BM, 1) && weights(&m1.B, a.W1, d, F, a.E) &&
+              make_map(&m2.A, 2, a.H8, F, all, 1, a.hF, 0, BM, 1) && weights(&m2.B, a.W2, F, d, a.E);
+    m1.B2 = m1.B;
+    if (ok && swiglu) ok = weights(&m1.B2, a.Wu, d, F, a.E);
+    m1.As = m1.A; m1.Bs = m1.B; m1.Bs2 = m1.B2;
+    m2.As = m2.A; m2.B2 = m2.Bs = m2.Bs2 = m2.B;
     if (ok && has_sh) {
-        ok = make_map(&A1s, 2, a.x, d, a.T, 1, d, 0, BM, 1) && make_map(&B1s, 3, a.Wsg, d, S, 1, d, 0, box1, 1) &&
-             make_map(&A2s, 2, a.H8, S, all, 1, a.hF, 0, BM, 1) && make_map(&B2s, 3, a.Wsd, S, d, 1, S, 0, BN, 1);
-        B1su = B1s;
-        if (ok && swiglu) ok = make_map(&B1su, 3, a.Wsu, d, S, 1, d, 0, box1, 1);
+        ok = make_map(&m1.As, 2, a.x, d, a.T, 1, d, 0, BM, 1) && weights(&m1.Bs, a.Wsg, d, S, 1) &&
+             make_map(&m2.As, 2, a.H8, S, all, 1, a.hF, 0, BM, 1) && weights(&m2.Bs, a.Wsd, S, d, 1);
+        m1.Bs2 = m1.Bs;
+        m2.Bs2 = m2.Bs;
+        if (ok && swiglu) ok = weights(&m1.Bs2, a.Wsu, d, S, 1);
     }
     if (!ok) return cudaErrorInvalidValue;
 
@@ -503,9 +783,9 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     p.out = a.H8; p.ldo = a.hF;
     p.out_scale = a.h_scale; p.ld_out_scale = a.ld_hs / 4;
     p.timeout_ns = 2000000000ull;
-    const int grid = a.num_sms;
-    cudaError_t e = swiglu ? launch_gemm<FB_SWIGLU>(A1, A1s, B1, B1u, B1s, B1su, p, grid, st, a.pdl)
-                           : launch_gemm<FB_GELU>(A1, A1s, B1, B1u, B1s, B1su, p, grid, st, a.pdl);
+    const bool few = a.routed_rows <= BM && (!has_sh || a.T <= BM);
+    cudaError_t e = swiglu ? launch_product<FB_SWIGLU>(m1, p, few, a.num_sms, st, a.pdl)
+                           : launch_product<FB_GELU>(m1, p, few, a.num_sms, st, a.pdl);
     if (e != cudaSuccess) return e;
 
     p.K_routed = a.F; p.K_shared = a.S; p.N_routed = a.d; p.N_shared = a.d;
@@ -516,7 +796,7 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     p.row_gate = a.row_gate;
     p.out = a.y_perm; p.ldo = a.d;
     p.out_scale = nullptr; p.ld_out_scale = 0;
-    return launch_gemm<FB_DOWN>(A2, A2s, B2, B2, B2s, B2s, p, grid, st, true);
+    return launch_product<FB_DOWN>(m2, p, few, a.num_sms, st, true);
 }
 
 }  // namespace moe
