@@ -43,15 +43,14 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128, BN = 256, BK = 128;
-constexpr int STAGES = 3;
+constexpr int STAGES = 4;
 constexpr int kThreads = 384;                // 3 warpgroups: control, 2 x sums
 constexpr uint32_t A_BYTES = BM * BK;
 constexpr uint32_t B_BYTES = BN * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kMaxGroups = 257;
-constexpr int BH = BN / 2;                          // columns of a unit: half a tile's
-constexpr uint32_t kIdesc = make_idesc_e4m3(BM, BH);
+constexpr uint32_t kIdesc = make_idesc_e4m3(BM, BN);
 
 enum { FB_SWIGLU = 0, FB_GELU = 1, FB_DOWN = 2 };
 
@@ -85,8 +84,8 @@ template <int NS>
 struct TailT {
     uint64_t full[NS];
     uint64_t empty[NS];
-    uint64_t accf[4];            // unit 2 * half + (K block & 1)
-    uint64_t acce[4];
+    uint64_t accf[2];
+    uint64_t acce[2];
     uint64_t drain[2];
     uint64_t xch[4];             // SwiGLU: both halves of a quadrant's rows left their maxima
     uint32_t tmem_base;
@@ -99,8 +98,8 @@ struct TailT {
     float amax[2][2][BM];        // SwiGLU: the two halves' row maxima, two tiles deep
 };
 using Tail = TailT<STAGES>;
-// Output staging: 32 rows of 256 bytes per sums warp.
-constexpr uint32_t STG_BYTES = 32 * 256;
+// Output staging: 32 rows of 64 bytes per sums warp.
+constexpr uint32_t STG_BYTES = 32 * 64;
 constexpr size_t kStgOff = (STAGES * STAGE_BYTES + sizeof(Tail) + 1023) / 1024 * 1024;
 constexpr size_t kSmemBytes = 1024 + kStgOff + 8 * STG_BYTES;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -153,36 +152,30 @@ __device__ __forceinline__ uint4 codes16(const float *v, float inv) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The warp's 32 rows of P 16-byte pieces through its staging buffer: each lane
-// writes its row, then neighbouring lanes store neighbouring pieces (stores by
-// row would touch 32 rows per instruction: 4096 more cycles a tile measured;
+// 64 bytes of each of the warp's 32 rows (w: this lane's row) through its staging
+// buffer to out + row * ld: four neighbouring lanes store a row's pieces (stores
+// by row would touch 32 rows per instruction: 4096 more cycles a tile measured;
 // TMA stores need a proxy fence, which waits 500 to 3000 cycles beside the
-// loads).  Piece p of row r lies at an XOR of p, so both sides are free of bank
-// conflicts.
-template <int P>
-__device__ __forceinline__ uint32_t piece_addr(uint32_t stg, int r, int p) {
-    const int x = P == 4 ? (p ^ ((r >> 1) & 3)) : (p ^ (r & 7));
-    return stg + r * (P * 16) + (x << 4);
-}
-template <int P>
-__device__ __forceinline__ void stage_put(uint32_t stg, int p, uint4 w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece_addr<P>(stg, threadIdx.x & 31, p)), "r"(w.x),
-                 "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-}
-// rows: valid rows of the warp; pieces: those below the row's end.
-template <int P>
-__device__ __forceinline__ void stage_out(uint32_t stg, char *out, int64_t ld, int rows, int pieces) {
-    const int lane = threadIdx.x & 31, p = lane % P;
-    __syncwarp();
+// loads).  Piece c of row r lies at c ^ ((r / 2) % 4), so both sides are free of
+// bank conflicts.  rows: valid rows of the warp; pieces: those below the row's end.
+__device__ __forceinline__ void stage_out(uint32_t stg, const uint4 (&w)[4], char *out, int64_t ld, int rows, int pieces) {
+    const int lane = threadIdx.x & 31, p = lane & 3;
+    __syncwarp();                                          // the last store has read the buffer
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int r = i * (32 / P) + lane / P;
-        uint4 w;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(piece_addr<P>(stg, r, p)) : "memory");
-        if (r < rows && p < pieces) *reinterpret_cast<uint4 *>(out + r * ld + p * 16) = w;
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t a = stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[c].x), "r"(w[c].y), "r"(w[c].z),
+                     "r"(w[c].w) : "memory");
     }
     __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stg + r * 64 + ((p ^ ((r >> 1) & 3)) << 4)) : "memory");
+        if (r < rows && p < pieces) *reinterpret_cast<uint4 *>(out + r * ld + p * 16) = v;
+    }
 }
 
 // What one sums thread knows of its tile: its output row and scale sources.
@@ -235,16 +228,21 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] += col0 + i < c.N ? __ldg(c.bias + col0 + i) : 0.f;
         }
+        char *o = static_cast<char *>(p.out) + (row0 * p.ldo + col0) * 2;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            uint4 w;
-            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&w);
+        for (int q = 0; q < 4; ++q) {
+            uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                h[i] = __floats2bfloat162_rn(acc[u * 8 + 2 * i] * c.gate, acc[u * 8 + 2 * i + 1] * c.gate);
-            stage_put<16>(stg, u, w);
+            for (int u = 0; u < 4; ++u) {
+                __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&w[u]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = q * 32 + u * 8 + 2 * i;
+                    h[i] = __floats2bfloat162_rn(acc[n] * c.gate, acc[n + 1] * c.gate);
+                }
+            }
+            stage_out(stg, w, o + q * 64, p.ldo * 2, rows, (c.N - col0) / 8 - q * 4);
         }
-        stage_out<16>(stg, static_cast<char *>(p.out) + (row0 * p.ldo + col0) * 2, p.ldo * 2, rows, (c.N - col0) / 8);
         return true;
     }
     constexpr int W = MODE == FB_SWIGLU ? 64 : 128;        // hidden values of this thread
@@ -280,9 +278,14 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
     }
     amax = fmaxf(amax, 0x1p-100f);
     const float inv = __fdiv_rn(448.f, amax);
+    char *o = static_cast<char *>(p.out) + row0 * p.ldo + col0;
 #pragma unroll
-    for (int u = 0; u < W / 16; ++u) stage_put<W / 16>(stg, u, codes16(acc + u * 16, inv));
-    stage_out<W / 16>(stg, static_cast<char *>(p.out) + row0 * p.ldo + col0, p.ldo, rows, (c.N - col0) / 16);
+    for (int q = 0; q < W / 64; ++q) {
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = codes16(acc + q * 64 + u * 16, inv);
+        stage_out(stg, w, o + q * 64, p.ldo, rows, (c.N - col0) / 16 - q * 4);
+    }
     if (!c.valid) return true;
     const int blk = MODE == FB_SWIGLU ? c.nt : c.nt * 2 + c.half;
     if ((MODE != FB_SWIGLU || c.half == 0) && blk * 128 < c.N)
@@ -351,6 +354,9 @@ __device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tm
     const int r_in_tile = q * 32 + lane;
     const uint32_t stg = stg0 + (uint32_t)(warp - 4) * STG_BYTES;
     const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
+    // columns of this warp: SwiGLU 64 gate and 64 up columns, else 128 in a row
+    const uint32_t c0 = MODE == FB_SWIGLU ? half * 64 : half * 128;
+    const uint32_t c1 = MODE == FB_SWIGLU ? 128 + half * 64 : half * 128 + 64;
     constexpr int TM = PAIR ? 2 * BM : BM;
     uint32_t cnt = 0;
     uint32_t flip = 0;                                     // parity of the tiles this CTA has done
@@ -371,26 +377,26 @@ __device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tm
         for (int i = 0; i < 128; ++i) acc[i] = 0.f;
         float ra = __ldg(c.sa), rw0 = __ldg(c.sw0), rw1 = __ldg(c.sw1);
         for (int kb = 0; kb < nk; ++kb, ++cnt) {
-            const uint32_t unit = (uint32_t)half * 2 + (cnt & 1u), aphase = (cnt >> 1) & 1u;
+            const uint32_t ab = cnt & 1u, aphase = (cnt >> 1) & 1u;
             const float s0 = ra * rw0, s1 = ra * rw1;
             if (kb + 1 < nk) {                             // the next block's scales arrive during this one
                 ra = __ldg(c.sa + kb + 1);
                 rw0 = __ldg(c.sw0 + kb + 1);
                 rw1 = MODE == FB_SWIGLU ? __ldg(c.sw1 + kb + 1) : rw0;
             }
-            if (!warp_wait(smem_u32(&s.accf[unit]), aphase, p.timeout_ns)) { if (lane == 0) fail(s, p, 64); ok = false; break; }
+            if (!warp_wait(smem_u32(&s.accf[ab]), aphase, p.timeout_ns)) { if (lane == 0) fail(s, p, 64); ok = false; break; }
             tc_fence_after();
-            const uint32_t ta = lane_addr + unit * BH;     // SwiGLU: 64 gate, then 64 up columns
+            const uint32_t ta = lane_addr + ab * BN;
             float v[64];
-            tmem_ld32x2(ta, ta + 32, v);
+            tmem_ld32x2(ta + c0, ta + c0 + 32, v);
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = fmaf(v[i], s0, acc[i]);
-            tmem_ld32x2(ta + 64, ta + 96, v);
+            tmem_ld32x2(ta + c1, ta + c1 + 32, v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {                               // the accumulator is free: its words are in registers
-                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[unit]), 0));
-                else mbar_arrive(smem_u32(&s.acce[unit]));
+                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[ab]), 0));
+                else mbar_arrive(smem_u32(&s.acce[ab]));
             }
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[64 + i] = fmaf(v[i], s1, acc[64 + i]);
@@ -420,8 +426,8 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     constexpr int BNO = MODE == FB_SWIGLU ? 128 : 256;     // output columns per tile
     if (tid == 0) {
         s.abort_flag = 0;
-        for (int i = 0; i < STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 2); }
-        for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 4); }
+        for (int i = 0; i < STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 8); }
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.xch[i]), 2);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -472,9 +478,9 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     mbar_arrive_expect_tx(fb, STAGE_BYTES);
                     tma_load_2d(smA + stage * A_BYTES, mA, fb, kb * BK, a_row);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)            // unit u / 2, its first or second 64 columns
-                        tma_load_3d(smB + stage * B_BYTES + u * (B_BYTES / 4), MODE == FB_SWIGLU && (u & 1) ? mB2 : mB, fb,
-                                    kb * BK, MODE == FB_SWIGLU ? nt * 128 + (u >> 1) * 64 : nt * BN + u * 64, e);
+                    for (int u = 0; u < 2; ++u)            // SwiGLU: 128 gate, then 128 up rows
+                        tma_load_3d(smB + stage * B_BYTES + u * (B_BYTES / 2), MODE == FB_SWIGLU && u ? mB2 : mB, fb,
+                                    kb * BK, MODE == FB_SWIGLU ? nt * 128 : nt * BN + u * 128, e);
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -484,39 +490,41 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (!mbar_wait(smem_u32(&s.full[i % STAGES]), (i / STAGES) & 1u, p.timeout_ns)) fail(s, p, 65);
         }
       } else if (warp < 3) {
-        // ================= MMA issuers: warp 1 the first unit of every K block,
-        // warp 2 the second, each alternating between two accumulators.  The
-        // whole warp runs the loop, so that descriptors stay in uniform
-        // registers; one lane issues (with a single-lane loop the issue took
-        // 500 cycles per K block beside the busy sums warps).
-        const uint32_t half = warp - 1;
+        // ================= MMA issuers: one accumulator per K block, warp 1 the
+        // even blocks, warp 2 the odd ones, so that one warp's waits and commits
+        // pass while the other's products run.  The whole warp runs the loop, so
+        // that descriptors stay in uniform registers; one lane issues (with a
+        // single-lane loop the issue took 500 cycles per K block beside the busy
+        // sums warps, now 70).
+        const uint32_t ab = warp - 1;
         const bool leader = elect_lane();
-        const uint64_t da0 = sdesc(smA), db0 = sdesc(smB + half * (B_BYTES / 2));
-        uint32_t i = 0;                                    // K blocks done
+        const uint64_t da0 = sdesc(smA), db0 = sdesc(smB);
+        const uint32_t dtm = tmem_base + ab * BN;
+        uint32_t cnt = 0;                                  // K blocks before this tile
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !aborted(s); tile += gridDim.x) {
             // the shared group, when there is one, is the last
-            const int nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
-            for (int kb = 0; kb < nk; ++kb, ++i) {
+            const uint32_t nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
+            uint32_t i = cnt + ((cnt ^ ab) & 1u);
+            cnt += nk;
+            for (; i < cnt; i += 2) {
                 const uint32_t stage = i % STAGES, phase = (i / STAGES) & 1u, aphase = (i >> 1) & 1u;
-                const uint32_t unit = half * 2 + (i & 1u);
-                if (!warp_wait(smem_u32(&s.acce[unit]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 62); ok = false; break; }
+                if (!warp_wait(smem_u32(&s.acce[ab]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 62); ok = false; break; }
                 if (!warp_wait(smem_u32(&s.full[stage]), phase, p.timeout_ns)) { if (leader) fail(s, p, 63); ok = false; break; }
                 tc_fence_after();
                 const uint64_t da = da0 + stage * (A_BYTES >> 4), db = db0 + stage * (B_BYTES >> 4);
-                const uint32_t dtm = tmem_base + unit * BH;
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k) mma_e4m3(dtm, da + k * 2, db + k * 2, kIdesc, k ? 1u : 0u);
-                    mma_commit(smem_u32(&s.accf[unit]));
+                    mma_commit(smem_u32(&s.accf[ab]));
                     mma_commit(smem_u32(&s.empty[stage]));
                 }
                 __syncwarp();
             }
         }
         if (aborted(s) && leader) {                        // products in flight end before TMEM is freed
-            mma_commit(smem_u32(&s.drain[half]));
-            if (!mbar_wait(smem_u32(&s.drain[half]), 0, p.timeout_ns)) fail(s, p, 66);
+            mma_commit(smem_u32(&s.drain[ab]));
+            if (!mbar_wait(smem_u32(&s.drain[ab]), 0, p.timeout_ns)) fail(s, p, 66);
         }
         __syncwarp();
       }
@@ -545,9 +553,9 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 // its full barriers collect both CTAs' copies, its commits reach both CTAs'
 // empty and accumulator-full barriers, and both CTAs' sums warps free the
 // accumulators at its barriers.
-constexpr int P_STAGES = 4;
+constexpr int P_STAGES = 6;
 constexpr uint32_t P_STAGE_BYTES = A_BYTES + B_BYTES / 2;
-constexpr uint32_t kIdescPair = make_idesc_e4m3(2 * BM, BH);
+constexpr uint32_t kIdescPair = make_idesc_e4m3(2 * BM, BN);
 using PairTail = TailT<P_STAGES>;
 constexpr size_t kPairStgOff = (P_STAGES * P_STAGE_BYTES + sizeof(PairTail) + 1023) / 1024 * 1024;
 constexpr size_t kPairSmemBytes = 1024 + kPairStgOff + 8 * STG_BYTES;
@@ -575,8 +583,8 @@ fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
 
     if (tid == 0) {
         s.abort_flag = 0;
-        for (int i = 0; i < P_STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 2); }
-        for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 8); }
+        for (int i = 0; i < P_STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 16); }
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.xch[i]), 2);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -614,9 +622,7 @@ fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                 const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + mt * 2 * BM + (int)rank * BM;
                 const CUtensorMap *mA = sh ? &tmAs : &tmA;
                 const CUtensorMap *mB = (MODE == FB_SWIGLU && rank == 1) ? (sh ? &tmBs2 : &tmB2) : (sh ? &tmBs : &tmB);
-                // this CTA's 64 rows of each unit's 128 (SwiGLU: gate or up)
-                const int b_row = MODE == FB_SWIGLU ? nt * 128 : nt * BN + (int)rank * 64;
-                constexpr int kUnitRows = MODE == FB_SWIGLU ? 64 : 128;
+                const int b_row = MODE == FB_SWIGLU ? nt * 128 : nt * BN + (int)rank * 128;
                 const int e = sh ? 0 : g;
                 for (int kb = 0; kb < nk; ++kb, ++i) {
                     const uint32_t stage = i % P_STAGES, phase = (i / P_STAGES) & 1u;
@@ -625,7 +631,6 @@ fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), 2 * P_STAGE_BYTES);
                     tma_load_2d_pair(smA + stage * A_BYTES, mA, fb, kb * BK, a_row);
                     tma_load_3d_pair(smB + stage * (B_BYTES / 2), mB, fb, kb * BK, b_row, e);
-                    tma_load_3d_pair(smB + stage * (B_BYTES / 2) + B_BYTES / 4, mB, fb, kb * BK, b_row + kUnitRows, e);
                 }
             }
             // every copy has landed before the pair may end: the last use of each stage
@@ -634,35 +639,36 @@ fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                     if (!mbar_wait(smem_u32(&s.full[j % P_STAGES]), (j / P_STAGES) & 1u, p.timeout_ns)) fail(s, p, 75);
         }
       } else if (warp < 3) {
-        // ================= MMA issuers (first CTA): first and second units
+        // ================= MMA issuers (first CTA): even and odd K blocks
         if (rank == 0) {
-            const uint32_t half = warp - 1;
+            const uint32_t ab = warp - 1;
             const bool leader = elect_lane();
-            const uint64_t da0 = sdesc(smA), db0 = sdesc(smB + half * (B_BYTES / 4));
-            uint32_t i = 0;
+            const uint64_t da0 = sdesc(smA), db0 = sdesc(smB);
+            const uint32_t dtm = tmem_base + ab * BN;
+            uint32_t cnt = 0;
             bool ok = true;
             for (int tile = pair; tile < total && ok && !aborted(s); tile += npairs) {
-                const int nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
-                for (int kb = 0; kb < nk; ++kb, ++i) {
+                const uint32_t nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
+                uint32_t i = cnt + ((cnt ^ ab) & 1u);
+                cnt += nk;
+                for (; i < cnt; i += 2) {
                     const uint32_t stage = i % P_STAGES, phase = (i / P_STAGES) & 1u, aphase = (i >> 1) & 1u;
-                    const uint32_t unit = half * 2 + (i & 1u);
-                    if (!warp_wait(smem_u32(&s.acce[unit]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 72); ok = false; break; }
+                    if (!warp_wait(smem_u32(&s.acce[ab]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 72); ok = false; break; }
                     if (!warp_wait(smem_u32(&s.full[stage]), phase, p.timeout_ns)) { if (leader) fail(s, p, 73); ok = false; break; }
                     tc_fence_after();
                     const uint64_t da = da0 + stage * (A_BYTES >> 4), db = db0 + stage * (B_BYTES >> 5);
-                    const uint32_t dtm = tmem_base + unit * BH;
                     if (leader) {
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k) mma_e4m3_pair(dtm, da + k * 2, db + k * 2, kIdescPair, k ? 1u : 0u);
-                        mma_commit_pair(smem_u32(&s.accf[unit]), (uint16_t)0x3);
+                        mma_commit_pair(smem_u32(&s.accf[ab]), (uint16_t)0x3);
                         mma_commit_pair(smem_u32(&s.empty[stage]), (uint16_t)0x3);
                     }
                     __syncwarp();
                 }
             }
             if (aborted(s) && leader) {                    // products in flight end before TMEM is freed
-                mma_commit_pair(smem_u32(&s.drain[half]), (uint16_t)0x1);
-                if (!mbar_wait(smem_u32(&s.drain[half]), 0, p.timeout_ns)) fail(s, p, 76);
+                mma_commit_pair(smem_u32(&s.drain[ab]), (uint16_t)0x1);
+                if (!mbar_wait(smem_u32(&s.drain[ab]), 0, p.timeout_ns)) fail(s, p, 76);
             }
             __syncwarp();
         }
@@ -750,9 +756,9 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     const uint64_t routed = a.routed_rows > 0 ? (uint64_t)a.routed_rows : 1;
     const uint64_t all = (uint64_t)(a.shared_base + (has_sh ? a.T : 0));
     const uint64_t d = a.d, F = a.F, S = a.S;
-    // weight boxes of 64 rows: half a unit, or a pair CTA's share of one
+    // weight boxes of 128 rows: half a tile, or a pair CTA's share of one
     auto weights = [](CUtensorMap *m, const uint8_t *w, uint64_t in, uint64_t out, uint64_t n) {
-        return make_map(m, 3, w, in, out, n, in, out * in, 64, 1);
+        return make_map(m, 3, w, in, out, n, in, out * in, 128, 1);
     };
     Maps m1, m2;
     bool ok = make_map(&m1.A, 2, a.x_perm, d, routed, 1, d, 0, BM, 1) && weights(&m1.B, a.W1, d, F, a.E) &&
