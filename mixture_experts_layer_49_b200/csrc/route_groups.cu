@@ -19,8 +19,13 @@
 //
 // One warp per token, lane l holding experts l * EPT .. l * EPT + EPT - 1, so
 // a group of 8 * 2^i experts is a power-of-two run of lanes and its best two
-// keys meet in a few shuffles.  The floor is the logits read once; the
-// selection's instructions bound it (k rounds of redux.sync).
+// keys meet in a few shuffles.  For the rounds of the choice a candidate is one
+// 32-bit word: the upper 24 bits of the fp32 distance of its key from the row's
+// largest, then its id, so one redux.sync.min finds the best candidate with the
+// lowest id, and a lane's candidates sort with plain minima and maxima.
+//
+// The floor is the logits read once (2.8 us for 16384 x 256); the selection's
+// instructions bound it.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -36,34 +41,27 @@ __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
     return v;
 }
-__device__ __forceinline__ float warp_min(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fminf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 
-// Order-preserving images of a key: 0 an expert that may not be chosen, 1 a
-// NaN key (below every number), else the number's.
-__device__ __forceinline__ uint32_t image(float f) {
-    if (f != f) return 1u;
-    f += 0.f;                                      // -0 and +0 are the same key
-    const uint32_t u = __float_as_uint(f);
+// Order-preserving image of a number; NaN counts as +inf.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f != f ? INFINITY : f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float number(uint32_t u) {
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
-}
+// The same of a key: 0 an expert that may not be chosen, 1 a NaN key (below every
+// number), else the number's.
 __device__ __forceinline__ uint64_t image(double f) {
     if (f != f) return 1ull;
-    f += 0.0;
+    f += 0.0;                                      // -0 and +0 are the same key
     const uint64_t u = (uint64_t)__double_as_longlong(f);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
+// fp64 keys decide; only fp32 keys are asked how close they are.
+template <typename F> __device__ __forceinline__ constexpr bool close_matters() { return sizeof(F) == 4; }
 
 template <typename F>
 __device__ __forceinline__ F low() { return (F)(-INFINITY); }
@@ -77,15 +75,21 @@ __device__ __forceinline__ void merge2(F &a, F &b, F oa, F ob) {
     b = b < lo ? lo : b;
 }
 
-// Which of this lane's experts lie in the topk_group best groups (bit j:
-// expert lane * EPT + j).  worst_kept / best_dropped: the two scores that the
-// decision lies between.
+// How far a group's score is off (an infinite one not at all).
+template <typename F>
+__device__ __forceinline__ F score_error(const RouteArgs &a, F score, F t1, F t2, F abs, F rel) {
+    if (!(fabs(score) < (F)INFINITY)) return (F)0;
+    return a.group_top == 2 ? (F)2 * abs + rel * (fabs(t1) + fabs(t2)) : abs + rel * fabs(t1);
+}
+
+// Which of this lane's experts lie in the topk_group best groups (bit j: expert
+// lane * EPT + j).  With keys off by at most abs + rel |key|: *close, whether a
+// kept and a dropped group's scores could be in the other order.
 template <int EPT, typename F>
-__device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&key)[EPT], F *worst_kept,
-                                                 F *best_dropped) {
+__device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&key)[EPT], F abs, F rel, bool *close) {
     const int lane = threadIdx.x & 31;
     const int size = a.E / a.n_group;
-    F wk = (F)INFINITY, bd = low<F>();
+    F wk = (F)INFINITY, bd = low<F>();             // least kept and greatest dropped score, error taken off and added
     uint32_t mask = 0;
     const int lanes = size / EPT;                  // lanes per group when a lane never spans two
     if (size % EPT == 0 && (lanes & (lanes - 1)) == 0) {
@@ -101,6 +105,7 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&k
         }
         F mine = a.group_top == 2 ? t1 + t2 : t1;
         if (mine != mine) mine = low<F>();         // +inf and -inf
+        const F err = score_error(a, mine, t1, t2, abs, rel);
         const int g = lane / lanes;
         int rank = 0;
         for (int q = 0; q < a.n_group; ++q) {
@@ -108,14 +113,14 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&k
             rank += (s > mine || (s == mine && q < g)) ? 1 : 0;
         }
         if (g < a.n_group) {
-            if (rank < a.topk_group) { mask = (1u << EPT) - 1u; wk = mine; } else { bd = mine; }
+            if (rank < a.topk_group) { mask = (1u << EPT) - 1u; wk = mine - err; } else { bd = mine + err; }
         }
     } else {
         // any size: group by group over the whole warp; lane q % 32 keeps the
         // scores of groups q, q + 32, ... (n_group <= 256)
-        F mine[8];
+        F mine[8], err[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mine[i] = low<F>();
+        for (int i = 0; i < 8; ++i) { mine[i] = low<F>(); err[i] = (F)0; }
         for (int q = 0; q < a.n_group; ++q) {
             F t1 = low<F>(), t2 = low<F>();
 #pragma unroll
@@ -132,7 +137,10 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&k
             if (s != s) s = low<F>();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (q == i * 32 + lane) mine[i] = s;
+                if (q == i * 32 + lane) {
+                    mine[i] = s;
+                    err[i] = score_error(a, s, t1, t2, abs, rel);
+                }
         }
         for (int q = 0; q < a.n_group; ++q) {
             F s = low<F>();
@@ -148,49 +156,46 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&k
                 if (p < a.n_group && (mine[i] > s || (mine[i] == s && p < q))) ++rank;
             }
             rank = __reduce_add_sync(kAll, rank);
-            if (rank < a.topk_group) {
-                wk = s < wk ? s : wk;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (q == i * 32 + lane) {
+                    if (rank < a.topk_group) wk = mine[i] - err[i] < wk ? mine[i] - err[i] : wk;
+                    else bd = mine[i] + err[i] > bd ? mine[i] + err[i] : bd;
+                }
+            if (rank < a.topk_group)
 #pragma unroll
                 for (int j = 0; j < EPT; ++j) {
                     const int e = lane * EPT + j;
                     if (e >= q * size && e < (q + 1) * size) mask |= 1u << j;
                 }
-            } else {
-                bd = s > bd ? s : bd;
-            }
         }
     }
-    *worst_kept = wk;
-    *best_dropped = bd;
+    *close = false;
+    if (close_matters<F>()) {                      // a NaN bound (infinite scores) compares false: not close
+        uint32_t lo = ordered((float)wk), hi = ordered((float)bd);
+        lo = __reduce_min_sync(kAll, lo);
+        hi = __reduce_max_sync(kAll, hi);
+        *close = lo < hi;
+    }
     return mask;
 }
 
-// Compare-exchange and sorting networks for a lane's candidates: key image
-// descending, then id ascending (ids ascend within a lane, networks keep the
-// order by comparing them).
-__device__ __forceinline__ void cex(uint32_t &ka, int &ia, uint32_t &kb, int &ib) {
-    const bool sw = ka < kb || (ka == kb && ia > ib);
-    const uint32_t tk = sw ? kb : ka;
-    kb = sw ? ka : kb;
-    ka = tk;
-    const int ti = sw ? ib : ia;
-    ib = sw ? ia : ib;
-    ia = ti;
-}
+// Ascending sorting networks of a lane's candidates (Batcher's odd-even merge
+// sort for 8).
 template <int EPT>
-__device__ __forceinline__ void lane_sort(uint32_t (&k)[EPT], int (&id)[EPT]) {
-#define CEX(i, j) cex(k[i], id[i], k[j], id[j])
+__device__ __forceinline__ void lane_sort(uint32_t (&v)[EPT]) {
+#define CEX(i, j) { const uint32_t lo = min(v[i], v[j]); v[j] = max(v[i], v[j]); v[i] = lo; }
     if constexpr (EPT == 2) {
-        CEX(0, 1);
+        CEX(0, 1)
     } else if constexpr (EPT == 4) {
-        CEX(0, 1); CEX(2, 3); CEX(0, 2); CEX(1, 3); CEX(1, 2);
+        CEX(0, 1) CEX(2, 3) CEX(0, 2) CEX(1, 3) CEX(1, 2)
     } else if constexpr (EPT == 8) {
-        CEX(0, 1); CEX(2, 3); CEX(4, 5); CEX(6, 7);
-        CEX(0, 2); CEX(1, 3); CEX(4, 6); CEX(5, 7);
-        CEX(1, 2); CEX(5, 6);
-        CEX(0, 4); CEX(1, 5); CEX(2, 6); CEX(3, 7);
-        CEX(2, 4); CEX(3, 5);
-        CEX(1, 2); CEX(3, 4); CEX(5, 6);
+        CEX(0, 1) CEX(2, 3) CEX(4, 5) CEX(6, 7)
+        CEX(0, 2) CEX(1, 3) CEX(4, 6) CEX(5, 7)
+        CEX(1, 2) CEX(5, 6)
+        CEX(0, 4) CEX(1, 5) CEX(2, 6) CEX(3, 7)
+        CEX(2, 4) CEX(3, 5)
+        CEX(1, 2) CEX(3, 4) CEX(5, 6)
     }
 #undef CEX
 }
@@ -252,8 +257,8 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int t) {
         key[j] = a.score == MOE_SCORE_SOFTMAX ? l : 1.0 / (1.0 + exp(-l));
         if (a.sel_bias && lane * EPT + j < a.E) key[j] += (double)a.sel_bias[lane * EPT + j];
     }
-    double wk, bd;
-    const uint32_t mask = kept_experts<EPT, double>(a, key, &wk, &bd);
+    bool close;
+    const uint32_t mask = a.topk_group < a.n_group ? kept_experts<EPT, double>(a, key, 0.0, 0.0, &close) : kAll;
     uint64_t im[EPT];
 #pragma unroll
     for (int j = 0; j < EPT; ++j) im[j] = (lane * EPT + j < a.E && (mask >> j & 1u)) ? image(key[j]) : 0ull;
@@ -313,20 +318,102 @@ __device__ __forceinline__ float of_expert(const float (&v)[EPT], int e) {
     return f;
 }
 
+// Largest value over the warp (NaN only where every lane holds one).
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 1 / (1 + exp(-l)): ex2 and rcp approximations, flushing below 2^-126.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
+}
+// The distance in a candidate's word.
+__device__ __forceinline__ float distance(uint32_t word) { return __uint_as_float(word & 0x7fffff00u); }
+
+// The topk_group best groups where a lane's candidates (sorted, best first)
+// belong to one group and a group is `lanes` (a power of two) neighbouring
+// lanes: the sum of a group's best distances, its id in the low 8 bits, and one
+// redux per kept group.  Whether this lane's group is kept; *close as above.
+template <int EPT>
+__device__ __forceinline__ bool kept_lane(const RouteArgs &a, int lanes, const uint32_t (&v)[EPT], float tol0, float tol_rel,
+                                          bool *close) {
+    const int lane = threadIdx.x & 31;
+    uint32_t t1 = v[0], t2 = EPT > 1 ? v[EPT > 1 ? 1 : 0] : kAll;
+    for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kAll, t1, o), o2 = __shfl_xor_sync(kAll, t2, o);
+        t2 = min(max(t1, o1), min(t2, o2));
+        t1 = min(t1, o1);
+    }
+    // a NaN distance (NaN key) counts as +inf, as in the exact selection
+    const float d = fminf(distance(t1), INFINITY) + (a.group_top == 2 ? fminf(distance(t2), INFINITY) : 0.f);
+    const int g = lane / lanes;
+    uint32_t word = g < a.n_group ? (__float_as_uint(d) & 0x7fffff00u) | (uint32_t)g : kAll;
+    bool kept = false;
+    uint32_t top = kAll;
+    for (int r = 0; r < a.topk_group; ++r) {
+        top = __reduce_min_sync(kAll, word);
+        if (word == top) { kept = true; word = kAll; }
+    }
+    const float last = distance(top), next = distance(__reduce_min_sync(kAll, word));
+    // two keys a score; each distance and the sum cut off at 2^-15
+    *close = next - last < 2.f * tol0 + 2.f * tol_rel * next;
+    return kept;
+}
+
+// The best a.k of n <= 31 candidates (lane r < n holds one) by their 64-bit keys:
+// lane r's chosen id of rank r.
+__device__ __noinline__ int rank_exact(const RouteArgs &a, int t, uint32_t mine, int n) {
+    const int lane = threadIdx.x & 31;
+    const int id = lane < n ? (int)(mine & 255u) : 0;
+    const float *p = a.logits + (size_t)t * a.E + id;
+    float h = p[0];
+    for (int s = 1; s < a.splits; ++s) h += p[(size_t)s * a.T * a.E];
+    double key = a.score == MOE_SCORE_SOFTMAX ? (double)h : 1.0 / (1.0 + exp(-(double)h));
+    if (a.sel_bias) key += (double)a.sel_bias[id];
+    const uint64_t im = image(key);
+    int rank = 0;
+    for (int q = 0; q < n; ++q) {
+        const uint64_t o = __shfl_sync(kAll, im, q);
+        const int oid = __shfl_sync(kAll, id, q);
+        rank += (o > im || (o == im && oid < id)) ? 1 : 0;
+    }
+    if (lane >= n) rank = 31;
+    int chosen = 0;
+    for (int q = 0; q < n; ++q) {
+        const int r = __shfl_sync(kAll, rank, q), oid = __shfl_sync(kAll, id, q);
+        if (r == lane) chosen = oid;
+    }
+    return lane < a.k ? chosen : 0;
+}
+
 template <int EPT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) route_select_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __grid_constant__ RouteArgs a) {
     pdl_wait_then_release();
-    __shared__ float part[WARPS][EPT * 32];
+    __shared__ __align__(16) float part[WARPS][EPT * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    const int size = a.E / a.n_group;
+    const int lanes = size % EPT == 0 && ((size / EPT) & (size / EPT - 1)) == 0 ? size / EPT : 0;   // 0: groups end inside lanes
     float sb[EPT], share[EPT];
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
         sb[j] = (a.sel_bias && lane * EPT + j < a.E) ? __ldg(a.sel_bias + lane * EPT + j) : 0.f;
         share[j] = 0.f;
     }
+    // Error of a key.  Sigmoid: ex2 of a rounded product is off by (2 + 1.2 |l|) ulp,
+    // which moves s by s (1 - s) of that, at most 1.3 * 2^-24; the sum rounds by
+    // 2^-24, rcp by an ulp: together below 4.3 * 2^-24 (s <= 1); the sum with the
+    // bias by 2^-24 of it.  Softmax: the latter alone.
+    const float err_abs = softmax ? 0.f : 0x1p-21f;
+    const float err_rel = (softmax && !a.sel_bias) ? 0.f : 0x1p-23f;
+    // Two distances: cut off at 2^-15 of them and one rounding, besides the keys.
+    const float tol_rel = 0x1.2p-14f + 2.f * err_rel;
     for (int i = 0; i < kBlockTok / WARPS; ++i) {
-        const int t = blockIdx.x * kBlockTok + warp * (kBlockTok / WARPS) + i;
+        const int t = blockIdx.x * kBlockTok + i * WARPS + warp;
         if (t >= a.T) break;                       // uniform over the warp
         float h[EPT], s[EPT], key[EPT];
         load_logits<EPT>(a, t, h);
@@ -335,71 +422,111 @@ __global__ void __launch_bounds__(WARPS * 32) route_select_kernel(const __grid_c
             for (int j = 0; j < EPT; ++j)
                 if (lane * EPT + j < a.E) a.logits_out[(size_t)t * a.E + lane * EPT + j] = h[j];
         }
-        const float inv = scores<EPT>(a.score, a.E, h, s);
-        // Error bounds of a key.  Sigmoid: expf within 2 ulp moves s by at most
-        // s (1 - s) 2^-22 <= 2^-24, the sum and the quotient round by 2^-24
-        // each, so 3 * 2^-24, plus half an ulp of the sum with the bias;
-        // softmax: half an ulp of that sum.  Two keys further apart than twice
-        // the bound (here taken 2.6 times and 2 times wider) are in order.
-        const float tol_abs = softmax ? 0.f : 0x1p-20f;
-        const float tol_rel = (softmax && !a.sel_bias) ? 0.f : 0x1p-22f;
+        float inv, mx;
+        if (softmax) {
+            inv = scores<EPT>(a.score, a.E, h, s);
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            share[j] += s[j] * inv;
-            if (softmax) s[j] *= inv;
-            const float k0 = softmax ? h[j] : s[j];
-            key[j] = a.sel_bias ? k0 + sb[j] : k0;
-        }
-        bool close = false;
-        uint32_t mask = kAll;
-        if (a.n_group > 1 && a.topk_group < a.n_group) {
-            float wk, bd, most = 0.f;
-            mask = kept_experts<EPT, float>(a, key, &wk, &bd);
-#pragma unroll
-            for (int j = 0; j < EPT; ++j)
-                if (fabsf(key[j]) < INFINITY) most = fmaxf(most, fabsf(key[j]));
-            most = warp_max(most);
-            wk = warp_min(wk);
-            bd = warp_max(bd);
-            // a score sums two keys of at most `most`: per score the bounds of
-            // both and a rounding of 2^-24 * 2 most, 2^-21 most for two scores
-            close = wk - bd < 2.f * tol_abs + 0x1p-20f * most;
-        }
-        uint32_t im[EPT];
-        int id[EPT];
-#pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            id[j] = lane * EPT + j;
-            im[j] = (id[j] < a.E && (mask >> j & 1u)) ? image(key[j]) : 0u;
-        }
-        lane_sort<EPT>(im, id);
-        int my_id = 0;
-        float before = 0.f;
-        for (int r = 0; r <= a.k; ++r) {           // round k only looks at the best key left out
-            const uint32_t top = __reduce_max_sync(kAll, im[0]);
-            if (r > 0 && top > 1u) {
-                const float now = number(top);
-                close = close || before - now < tol_abs + tol_rel * fmaxf(fabsf(before), fabsf(now));
+            for (int j = 0; j < EPT; ++j) {
+                s[j] *= inv;
+                share[j] += s[j];
+                key[j] = h[j] + sb[j];             // absent experts: -inf
             }
-            if (r == a.k || top == 0u) break;
-            before = top == 1u ? -INFINITY : number(top);
-            const uint32_t e = __reduce_min_sync(kAll, im[0] == top ? (uint32_t)id[0] : kAll);
-            if (lane == r) my_id = (int)e;
-            if (im[0] == top && (uint32_t)id[0] == e) {
+        } else {
+            float z = 0.f;
 #pragma unroll
-                for (int j = 0; j + 1 < EPT; ++j) { im[j] = im[j + 1]; id[j] = id[j + 1]; }
-                im[EPT - 1] = 0u;
-                id[EPT - 1] = 0x7fffffff;
+            for (int j = 0; j < EPT; ++j) { s[j] = fast_sigmoid(h[j]); z += s[j]; }      // absent experts: 0
+            z = warp_sum(z);
+            inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) {
+                share[j] = fmaf(s[j], inv, share[j]);
+                key[j] = lane * EPT + j < a.E ? s[j] + sb[j] : -INFINITY;
             }
         }
-        if (close) my_id = select_exact<EPT>(a, t);      // uniform: every lane sees the same keys
-        const float g = of_expert<EPT>(s, my_id);
-        float f = a.gate_scale;
+        mx = key[0];
+#pragma unroll
+        for (int j = 1; j < EPT; ++j) mx = fmaxf(mx, key[j]);
+        mx = redux_max(mx);
+        bool close = !(fabsf(mx) < INFINITY);      // an infinite best key: distances say nothing
+        // candidates: 24 bits of the distance from the best key (a NaN key's is NaN,
+        // above all others), then the id
+        uint32_t v[EPT];
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const uint32_t e = lane * EPT + j;
+            v[j] = e < (uint32_t)a.E ? (__float_as_uint(mx - key[j]) & 0x7fffff00u) | e : kAll;
+        }
+        // (2^-140: what the cut takes off a subnormal distance)
+        const float tol0 = 2.f * err_abs + 2.f * err_rel * fabsf(mx) + 0x1p-140f;
+        bool c = false;
+        if (a.topk_group == a.n_group) {
+            lane_sort<EPT>(v);
+        } else if (lanes) {
+            lane_sort<EPT>(v);
+            bool kept = kept_lane<EPT>(a, lanes, v, tol0, tol_rel, &c);
+            if (c)                                 // too close for cut-off distances: whole fp32 keys
+                kept = kept_experts<EPT, float>(a, key, err_abs, softmax ? 0x1p-22f : 2.f * err_rel, &c) != 0u;
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) v[j] = kept ? v[j] : kAll;
+        } else {
+            // two roundings more per score than per key, both within rel
+            const uint32_t mask = kept_experts<EPT, float>(a, key, err_abs, softmax ? 0x1p-22f : 2.f * err_rel, &c);
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) v[j] = mask >> j & 1u ? v[j] : kAll;
+            lane_sort<EPT>(v);
+        }
+        // k rounds: the best candidate over the warp leaves its lane's list; lane r
+        // keeps the winner of round r, lane k (or `next`) the best one left out
+        uint32_t mine = kAll;
+        for (int r = 0; r < a.k; ++r) {
+            const uint32_t top = __reduce_min_sync(kAll, v[0]);
+            const bool win = v[0] == top;
+#pragma unroll
+            for (int j = 0; j + 1 < EPT; ++j) v[j] = win ? v[j + 1] : v[j];
+            v[EPT - 1] = win ? kAll : v[EPT - 1];
+            mine = lane == r ? top : mine;
+        }
+        uint32_t next = __reduce_min_sync(kAll, v[0]);
+        uint32_t after = __shfl_down_sync(kAll, mine, 1);
+        if (lane == a.k - 1) after = next;
+        // an infinite or NaN distance compares false: not close, ids decide
+        const bool tight = lane < a.k && after != kAll && distance(after) - distance(mine) < tol0 + tol_rel * distance(after);
+        int my_id = lane < a.k ? (int)(mine & 255u) : 0;
+        close = close || c;
+        if (!close && __any_sync(kAll, tight)) {
+            // the chosen and whatever lies within the bound behind them, one to a
+            // lane, ranked by their 64-bit keys
+            const float limit = distance(__shfl_sync(kAll, mine, a.k - 1));
+            int n = a.k;
+            while (n < 32 && next != kAll && distance(next) - limit < tol0 + tol_rel * distance(next)) {
+                const bool win = v[0] == next;
+#pragma unroll
+                for (int j = 0; j + 1 < EPT; ++j) v[j] = win ? v[j + 1] : v[j];
+                v[EPT - 1] = win ? kAll : v[EPT - 1];
+                mine = lane == n ? next : mine;
+                ++n;
+                next = __reduce_min_sync(kAll, v[0]);
+            }
+            if (n == 32) close = true;             // maybe more than lanes
+            else my_id = rank_exact(a, t, mine, n);
+        }
+        if (close) my_id = select_exact<EPT>(a, t);
+        // the chosen scores by id, through the warp's row of `part`
+        if constexpr (EPT >= 4) {
+#pragma unroll
+            for (int j = 0; j < EPT; j += 4)
+                *reinterpret_cast<float4 *>(&part[warp][lane * EPT + j]) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) part[warp][lane * EPT + j] = s[j];
+        }
+        __syncwarp();
+        const float g = part[warp][my_id];
+        __syncwarp();
+        float f = g * a.gate_scale;
         if (!softmax || a.renorm) {
             const float sum = warp_sum(lane < a.k ? g : 0.f);
             f = sum == 0.f ? 0.f : g / sum * a.gate_scale;   // no scores left: gates of 0
-        } else {
-            f = g * a.gate_scale;
         }
         if (lane < a.k) {
             a.idx[(size_t)t * a.k + lane] = my_id;
@@ -501,7 +628,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     }
 }
 
-constexpr int kSelWarps = 32;
+constexpr int kSelWarps = 16;
 
 // A row of E fp32 values splits into whole aligned vectors of the lanes.
 int vector_rows(const void *p, int E) {
