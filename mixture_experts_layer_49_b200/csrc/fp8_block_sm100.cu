@@ -753,6 +753,7 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     const bool swiglu = a.act == MOE_ACT_SWIGLU;
     const bool has_sh = a.S > 0 && a.T > 0;
     if (a.routed_rows == 0 && !has_sh) return cudaSuccess;
+    if (a.T <= kFp8BlockDecodeT) return launch_ffn_fp8_block_decode(a, st);
     const uint64_t routed = a.routed_rows > 0 ? (uint64_t)a.routed_rows : 1;
     const uint64_t all = (uint64_t)(a.shared_base + (has_sh ? a.T : 0));
     const uint64_t d = a.d, F = a.F, S = a.S;

@@ -362,6 +362,7 @@ struct FfnFp8BlockArgs {
     const float *b1, *b2;                             // GELU biases or null
     uint8_t *H8; float *h_scale;                      // [routed_rows (+T), hF] codes, scale rows
     int64_t ld_hs;                                    // bytes
+    float *h32;                                       // [rows, hF] fp32 hidden rows (at most kFp8BlockDecodeT tokens)
     __nv_bfloat16 *y_perm;                            // [routed_rows (+T), d]
     int32_t *status;
     int T, d, E, F, S, act, hF;
@@ -370,6 +371,12 @@ struct FfnFp8BlockArgs {
     bool pdl;
 };
 cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st);
+// The form for one or two tokens (fp8_block_decode.cu).  Measured against the tile
+// kernels, us: Qwen3 shape T 1 14.6 / 26.3, T 2 25.3 / 32.2, T 8 69.7 / 63.1; 32
+// experts of 7168 x 2048 and a shared one T 1 86 / 89, T 4 245 / 198; Mixtral shape
+// T 1 84 / 139, T 4 248 / 238.
+constexpr int kFp8BlockDecodeT = 2;
+cudaError_t launch_ffn_fp8_block_decode(const FfnFp8BlockArgs &a, cudaStream_t st);
 
 // ---- backward pass (bwd_sm100.cu, bwd_aux.cu)
 // One grouped GEMM C = A B^T on the tensor cores, bf16 operands, fp32

@@ -45,6 +45,7 @@ struct Layout {
     // e4m3 experts with a scale per block of 128 (codes in x8, x_perm and H8
     // as above): scale rows of x, of the packed rows and of H
     size_t xs, xs_perm, hs;
+    size_t h32;          // fp32 hidden rows of a few tokens
     size_t total;
 };
 
@@ -88,6 +89,7 @@ Layout layout(const moe_config *c) {
     L.xs = o;         o = align256(o + f8 * (size_t)c->T * scale_row_bytes(c->d_model));
     L.xs_perm = o;    o = align256(o + f8 * Tk * scale_row_bytes(c->d_model));
     L.hs = o;         o = align256(o + f8 * rows * scale_row_bytes((int)hF));
+    L.h32 = o;        o = align256(o + (c->T <= moe::kFp8BlockDecodeT ? f8 * rows * hF * 4 : 0));
     L.total = o;
     return L;
 }
@@ -985,6 +987,7 @@ static moe::FfnFp8BlockArgs fp8_block_args(const moe_config *cfg, const uint8_t 
     a.H8 = at<uint8_t>(ws, L.H8);
     a.h_scale = at<float>(ws, L.hs);
     a.ld_hs = (int64_t)scale_row_bytes(a.hF);
+    a.h32 = at<float>(ws, L.h32);
     a.y_perm = static_cast<__nv_bfloat16 *>(y_perm);
     a.status = status_word(ws);
     a.T = cfg->T; a.d = cfg->d_model; a.E = cfg->E; a.F = cfg->d_ff; a.S = cfg->d_ff_shared; a.act = cfg->act;

@@ -710,40 +710,49 @@ def forward_fp8(cfg, inp, w8, out: Outputs, ws, stream=None):
 
 
 # ---------------------------------------------------------------- experts in e4m3 with a scale per block of 128
-_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+# accepted types of an argument
+_F32, _I32, _BF16, _F64, _U8 = (torch.float32,), (torch.int32,), (torch.bfloat16,), (torch.float64,), (torch.uint8,)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _current_device() -> int:
-    if not torch.cuda.is_available():
-        raise ValueError("libmoe takes device tensors; there is no CUDA device")
-    return torch.cuda.current_device()
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError) as e:
+        raise ValueError("libmoe takes device tensors; there is no CUDA device") from e
 
 
-def _arg(t, name, dev, dtypes, numel=None):
+def _arg(t, name, dev, dtypes, numel=0):
     """Device pointer of an argument (None -> NULL): a contiguous tensor of one
-    of `dtypes` on the current device, holding at least `numel` elements."""
+    of the types `dtypes` on the current device, holding at least `numel`
+    elements."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s: expected a torch.Tensor" % name)
+    try:
+        if t.get_device() == dev and t.dtype in dtypes and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError("%s: expected a torch.Tensor" % name) from None
     if not t.is_cuda:
         raise ValueError("%s: libmoe takes device tensors; got one on %s" % (name, t.device))
     if t.get_device() != dev:
         raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), dev))
-    if t.dtype is not dtypes and (not isinstance(dtypes, tuple) or t.dtype not in dtypes):
-        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtypes))
+    if t.dtype not in dtypes:
+        raise ValueError("%s: %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
     if not t.is_contiguous():
         raise ValueError("%s: libmoe takes contiguous tensors" % name)
-    if numel is not None and t.numel() < numel:
-        raise ValueError("%s holds %d elements, %d are needed" % (name, t.numel(), numel))
-    return t.data_ptr()
+    raise ValueError("%s holds %d elements, %d are needed" % (name, t.numel(), numel))
+
+
+# the current stream's handle without building a Stream object, which costs as
+# much as a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _cu_stream(stream, dev):
     """The stream's handle: the current one, or one of the current device."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev)
     if stream.device_index != dev:
         raise ValueError("the stream is on cuda:%d, the current device is cuda:%d" % (stream.device_index, dev))
     return stream.cuda_stream
@@ -809,7 +818,7 @@ def moe_grouped_ffn_fp8_block(cfg, x8_perm, xs_perm, offsets, row_gate, w, b1, b
         _arg(row_gate, "row_gate", dev, _F32, rows), ctypes.byref(w), _arg(b1, "b1", dev, _F32, E * cfg.d_ff),
         _arg(b2, "b2", dev, _F32, E * d), _arg(x8, "x8", dev, _CODES, T * d), _arg(xs, "xs", dev, _F32, T * spr),
         _arg(y_perm, "y_perm", dev, _BF16, (rows + (T if cfg.d_ff_shared else 0)) * d),
-        _arg(ws, "ws", dev, torch.uint8), ws.numel(), _cu_stream(stream, dev)), "moe_grouped_ffn_fp8_block")
+        _arg(ws, "ws", dev, _U8), ws.numel(), _cu_stream(stream, dev)), "moe_grouped_ffn_fp8_block")
 
 
 def moe_forward_fp8_block(cfg, groups, x, x8, xs, Wr, logit_bias, sel_bias, w, b1, b2, y, idx, gate, counts, f, P,
@@ -824,9 +833,9 @@ def moe_forward_fp8_block(cfg, groups, x, x8, xs, Wr, logit_bias, sel_bias, w, b
         _arg(sel_bias, "sel_bias", dev, _F32, E), ctypes.byref(w), _arg(b1, "b1", dev, _F32, E * cfg.d_ff),
         _arg(b2, "b2", dev, _F32, E * d), _arg(y, "y", dev, _BF16, T * d), _arg(idx, "idx", dev, _I32, T * k),
         _arg(gate, "gate", dev, _F32, T * k), _arg(counts, "counts", dev, _I32, E), _arg(f, "f", dev, _F32, E),
-        _arg(P, "P", dev, _F32, E), _arg(loss, "loss", dev, torch.float64, 1),
+        _arg(P, "P", dev, _F32, E), _arg(loss, "loss", dev, _F64, 1),
         _arg(logits_out, "logits_out", dev, _F32, T * E), _arg(n_dropped, "n_dropped", dev, _I32, 1),
-        _arg(ws, "ws", dev, torch.uint8), ws.numel(), _cu_stream(stream, dev)), "moe_forward_fp8_block")
+        _arg(ws, "ws", dev, _U8), ws.numel(), _cu_stream(stream, dev)), "moe_forward_fp8_block")
 
 
 def forward_fp8_block(cfg, inp, w, sld, out: Outputs, ws, stream=None, groups=None, x8=None, xs=None):
@@ -876,9 +885,9 @@ def moe_router_topk_groups(cfg, groups, x, Wr, logit_bias, sel_bias, idx, gate, 
 
 # ---------------------------------------------------------------- RMS norm
 def _norm_dtype(t):
-    if t.dtype is _BF16:
+    if t.dtype is torch.bfloat16:
         return MOE_BF16
-    if t.dtype is _F32:
+    if t.dtype is torch.float32:
         return MOE_F32
     raise ValueError("RMS norm takes bf16 or fp32 rows, got %s" % t.dtype)
 
@@ -890,7 +899,7 @@ def moe_rmsnorm(x, residual, weight, eps, h, y, codes=None, scale=None, stream=N
     and codes with scale may each be None."""
     dev = _current_device()
     rows, d = x.shape
-    dt, n = x.dtype, rows * d
+    dt, n = (x.dtype,), rows * d
     ld = 0
     if scale is not None:
         ld = scale.shape[-1] * 4
@@ -917,9 +926,9 @@ def moe_rmsnorm_backward(h, weight, eps, dy, dres, dh, dweight, ws, stream=None)
     dres, the gradient from the residual stream, may be None) and dweight fp32."""
     dev = _current_device()
     rows, d = h.shape
-    dt, n = h.dtype, rows * d
+    dt, n = (h.dtype,), rows * d
     _check(lib().moe_rmsnorm_backward(
         _norm_dtype(h), rows, d, _arg(h, "h", dev, dt), _arg(weight, "weight", dev, _F32, d), eps,
         _arg(dy, "dy", dev, dt, n), _arg(dres, "dres", dev, dt, n), _arg(dh, "dh", dev, dt, n),
-        _arg(dweight, "dweight", dev, _F32, d), _arg(ws, "ws", dev, torch.uint8), ws.numel(),
+        _arg(dweight, "dweight", dev, _F32, d), _arg(ws, "ws", dev, _U8), ws.numel(),
         _cu_stream(stream, dev)), "moe_rmsnorm_backward")

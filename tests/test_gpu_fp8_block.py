@@ -106,6 +106,19 @@ CASES = [
     (40, 144, 2, 2064, 1, "swiglu", 0, [17, 12]),                            # capacity dropped 11 rows
     (64, 256, 2, 256, 2, "swiglu", 0, [0, 0]),                               # no row kept
     (600, 256, 3, 272, 2, "swiglu", 128, [257, 384, 513]),
+    # a few tokens: one pass of eight rows, more rows than tokens, widths that end inside a block
+    (8, 2048, 64, 768, 8, "swiglu", 0, [1] * 64),
+    (8, 272, 3, 144, 2, "gelu", 272, [9, 0, 7]),
+    (3, 1040, 40, 400, 2, "swiglu", 16, [0] * 33 + [1, 0, 3, 0, 0, 0, 2]),
+    (7, 400, 8, 272, 8, "swiglu", 0, [33, 20, 0, 0, 0, 0, 1, 0]),
+    (9, 272, 3, 144, 2, "gelu", 272, [9, 0, 9]),
+    # one and two tokens: single rows, all rows on one expert (more than one pass), none kept
+    (1, 2048, 64, 768, 8, "swiglu", 0, [1] * 8 + [0] * 56),
+    (2, 2048, 64, 768, 8, "swiglu", 0, [0] * 40 + [1, 2] * 5 + [0] * 14),
+    (2, 272, 8, 144, 8, "gelu", 272, [9, 0, 0, 0, 0, 0, 0, 7]),
+    (2, 400, 8, 272, 8, "swiglu", 16, [0, 16, 0, 0, 0, 0, 0, 0]),
+    (2, 1040, 40, 2064, 2, "swiglu", 16, [0] * 33 + [1, 0, 2, 0, 0, 0, 0]),
+    (2, 16, 2, 16, 1, "gelu", 0, [0, 0]),
 ]
 
 
