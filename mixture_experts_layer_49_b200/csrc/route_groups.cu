@@ -306,16 +306,33 @@ __device__ __forceinline__ float scores(int score, int E, const float (&h)[EPT],
     return z == 0.f ? 0.f : 1.f / z;
 }
 
-// v of expert e (lane e / EPT, register e % EPT) for every lane's own e.
+// A lane's registers to and from its warp's row in shared memory.
 template <int EPT>
-__device__ __forceinline__ float of_expert(const float (&v)[EPT], int e) {
-    float f = 0.f;
+__device__ __forceinline__ void put_row(float *row, const float (&v)[EPT]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (EPT >= 4) {
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-        const float t = __shfl_sync(kAll, v[j], (e / EPT) & 31);
-        if (e % EPT == j) f = t;
+        for (int j = 0; j < EPT; j += 4)
+            *reinterpret_cast<float4 *>(row + lane * EPT + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) row[lane * EPT + j] = v[j];
     }
-    return f;
+    __syncwarp();
+}
+template <int EPT>
+__device__ __forceinline__ void get_row(const float *row, float (&v)[EPT]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (EPT >= 4) {
+#pragma unroll
+        for (int j = 0; j < EPT; j += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(row + lane * EPT + j);
+            v[j] = f.x; v[j + 1] = f.y; v[j + 2] = f.z; v[j + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) v[j] = row[lane * EPT + j];
+    }
 }
 
 // Largest value over the warp (NaN only where every lane holds one).
@@ -512,15 +529,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __gri
         }
         if (close) my_id = select_exact<EPT>(a, t);
         // the chosen scores by id, through the warp's row of `part`
-        if constexpr (EPT >= 4) {
-#pragma unroll
-            for (int j = 0; j < EPT; j += 4)
-                *reinterpret_cast<float4 *>(&part[warp][lane * EPT + j]) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < EPT; ++j) part[warp][lane * EPT + j] = s[j];
-        }
-        __syncwarp();
+        put_row<EPT>(part[warp], s);
         const float g = part[warp][my_id];
         __syncwarp();
         float f = g * a.gate_scale;
@@ -534,8 +543,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __gri
         }
     }
     if (a.psum == nullptr) return;
-#pragma unroll
-    for (int j = 0; j < EPT; ++j) part[warp][lane * EPT + j] = share[j];
+    put_row<EPT>(part[warp], share);
     __syncthreads();
     for (int e = tid; e < a.E; e += WARPS * 32) {
         float v = 0.f;
@@ -551,7 +559,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __gri
 template <int EPT>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     pdl_wait_then_release();
+    __shared__ __align__(16) float rows[8][EPT * 32];          // a warp's row: scores, then their gradients
     const int lane = threadIdx.x & 31;
+    float *row = rows[threadIdx.x >> 5];
     const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (t >= a.T) return;
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
@@ -573,20 +583,28 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
         if (softmax) s[j] *= inv;
         ds[j] = 0.f;
     }
+    put_row<EPT>(row, s);
     if (!softmax || a.renorm) {
-        const float sv = of_expert<EPT>(s, e);
+        const float sv = row[e];
         const float sum = warp_sum(used ? sv : 0.f);
         const float g = sum == 0.f ? 0.f : sv / sum;
         const float dot = warp_sum(dg * g);
         dg = (used && sum != 0.f) ? (dg - dot) / sum : 0.f;
     }
-    for (int r = 0; r < a.k; ++r) {
-        const int er = __shfl_sync(kAll, e, r);
-        const float v = __shfl_sync(kAll, dg, r);
-#pragma unroll
-        for (int j = 0; j < EPT; ++j)
-            if (er == lane * EPT + j) ds[j] += v;
+    // the chosen experts' gradients to their lanes
+    __syncwarp();
+    put_row<EPT>(row, ds);
+    const uint32_t same = __match_any_sync(kAll, used ? e : -1 - lane);
+    if (__any_sync(kAll, (same & (same - 1u)) != 0u)) {        // an id twice: slots in order
+        for (int r = 0; r < a.k; ++r) {
+            if (lane == r && used) row[e] += dg;
+            __syncwarp();
+        }
+    } else {
+        if (used) row[e] = dg;
+        __syncwarp();
     }
+    get_row<EPT>(row, ds);
     if (a.alpha != 0.f) {
         const float c = (float)((double)a.alpha * a.E / a.T / ((double)a.T * a.k));
         float cf[EPT], dot = 0.f;
