@@ -29,7 +29,7 @@ moe_status check_norm(const char *where, int32_t dtype, int64_t rows, int32_t d,
 }
 
 size_t bwd_bytes(int64_t rows, int32_t d) {
-    return ((size_t)moe::rmsnorm_bwd_parts(rows) * (size_t)d * 4 + 256 + 255) / 256 * 256;
+    return ((size_t)moe::rmsnorm_bwd_parts(rows, d) * (size_t)d * 4 + 256 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -76,7 +76,7 @@ moe_status moe_rmsnorm_backward(int32_t dtype, int64_t rows, int32_t d, const vo
         return bad(MOE_ERR_WORKSPACE, where, "workspace smaller than moe_rmsnorm_backward_workspace_size()");
     moe::RmsNormBwdArgs a{};
     a.h = h; a.dy = dy; a.dres = dres; a.weight = weight; a.dh = dh; a.part = static_cast<float *>(ws);
-    a.dweight = dweight; a.rows = rows; a.d = d; a.eps = eps;
+    a.dweight = dweight; a.rows = rows; a.d = d; a.eps = eps; a.num_sms = moe::device_sms();
     return done(moe::launch_rmsnorm_bwd(a, dtype == MOE_BF16, reinterpret_cast<cudaStream_t>(stream)), where);
 }
 

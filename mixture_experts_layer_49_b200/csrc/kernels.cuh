@@ -292,14 +292,14 @@ struct RmsNormBwdArgs {
     const void *h, *dy, *dres;   // dres may be null
     const float *weight;
     void *dh;
-    float *part;                 // [rmsnorm_bwd_parts(rows), d] scratch
+    float *part;                 // [rmsnorm_bwd_parts(rows, d), d] scratch (at most)
     float *dweight;              // [d]
     int64_t rows;
-    int d;
+    int d, num_sms;
     float eps;
     bool pdl;
 };
-int64_t rmsnorm_bwd_parts(int64_t rows);
+int64_t rmsnorm_bwd_parts(int64_t rows, int d);
 cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs &a, bool bf16, cudaStream_t st);
 
 // ---- group-limited expert selection (route_groups.cu)
@@ -325,7 +325,8 @@ struct RouteBwdArgs {
     float *dlogits;              // [T, E]
     int T, E, k, score, renorm;
     float gate_scale, alpha;
-    int vec, vec_out;            // set by the launcher
+    float balance;               // set by the launcher, as vec and vec_out
+    int vec, vec_out;
     bool pdl;
 };
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, cudaStream_t st);
@@ -469,5 +470,6 @@ cudaError_t launch_set_pair(int32_t *p, int32_t a, int32_t b, cudaStream_t st); 
 moe_status validate_config(const moe_config *cfg);        // sets the error detail
 moe_status validate_groups(const moe_config *cfg, const moe_route_groups *g);
 void set_error_detail(const char *where, const char *what);
+int device_sms();                                         // of the current device
 
 }  // namespace moe

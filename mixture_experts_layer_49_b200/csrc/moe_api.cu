@@ -437,6 +437,8 @@ void forget_saved_preacts(const void *ws) {
     }
 }
 
+int device_sms() { return num_sms(); }
+
 void set_error_detail(const char *where, const char *what) {
     snprintf(g_detail, sizeof g_detail, "%s: %s", where, what);
 }

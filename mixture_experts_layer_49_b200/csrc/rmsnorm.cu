@@ -24,6 +24,8 @@
 // threads.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -31,7 +33,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kPartRows = 592;                 // rows of partial dw sums: 4 per SM
+constexpr int kPartRows = 592;                 // rows of partial dw sums at d >= 1024: 4 per SM
 
 template <typename T>
 struct Vec8;                                   // eight elements of a row as loaded
@@ -176,66 +178,91 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(RmsNormArgs a) {
     }
 }
 
-// One block per row at a time, rows blockIdx.x, blockIdx.x + gridDim.x, ...; the
-// next row's loads are in flight while this one is reduced (without: 76 us at
-// 16384 x 2048 bf16 against a floor of 41).  The block's share of dw stays in
-// registers and ends in part[blockIdx.x].
-template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1024 / MAXT) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
+// blockDim = (threads per row, rows at a time), rows of more than one warp one at a
+// time; part p of gridDim.x * blockDim.y takes rows p, p + parts, ...; its share of
+// dw stays in registers and ends in part[p].  The rows'
+// h, dy and dres come through shared memory by cp.async, STAGES rows ahead: each
+// thread copies and reads its own vectors, so nothing but its own wait orders
+// them, and 190 KB per SM are in flight at 16384 x 2048 bf16 (with one row held in
+// registers instead: 76 us; one row ahead in registers: 61 us; floor 41).  STAGES
+// 0: rows too wide for that, loaded as they are needed.
+template <typename T, int VPT, int MAXT, int STAGES>
+__global__ void __launch_bounds__(MAXT) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
     pdl_wait_then_release();
-    __shared__ float red[2][2][32];
+    extern __shared__ __align__(16) uint8_t stage_mem[];       // [STAGES][h, dy, dres][VPT * blockDim.x] vectors
+    __shared__ float2 red[2][32];
+    constexpr int VB = 8 * sizeof(T);             // bytes of a vector
     const int nvec = a.d >> 3, nw = blockDim.x >> 5;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, parts = (int64_t)gridDim.x * blockDim.y;
     const float inv_d = __fdiv_rn(1.f, (float)a.d);
-    float dw[VPT][8];
+    float dw[VPT][8], w[VPT][8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < VPT; ++i) {
+        const int v = min((int)(threadIdx.x + i * blockDim.x), nvec - 1);        // past the row: unused
+        Vec8<float> wv;
+        wv.load(a.weight + v * 8);
+        wv.get(w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-    Vec8<T> hv[VPT], gv[VPT], rv[VPT];
-    auto load = [&](int64_t row) {
-        const T *h = static_cast<const T *>(a.h) + row * a.d;
-        const T *dy = static_cast<const T *>(a.dy) + row * a.d;
-        const T *dres = static_cast<const T *>(a.dres) + row * a.d;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            const bool in = row < a.rows && v < nvec;
-            if (in) { hv[i].load(h + v * 8); gv[i].load(dy + v * 8); } else { hv[i].clear(); gv[i].clear(); }
-            if (in && a.dres) rv[i].load(dres + v * 8); else rv[i].clear();
-        }
+    }
+    auto src = [&](int which, int64_t row, int i) {
+        const void *base = which == 0 ? a.h : which == 1 ? a.dy : a.dres;
+        return static_cast<const T *>(base) + row * a.d + (threadIdx.x + i * blockDim.x) * 8;
     };
-    load(blockIdx.x);
-    int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-        Vec8<T> h[VPT], g[VPT], r[VPT];
+    auto slot = [&](int stage, int which, int i) {
+        return stage_mem + (size_t)((((stage * 3 + which) * VPT + i) * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x) * VB;
+    };
+    auto fetch = [&](int stage, int64_t row) {    // this thread's vectors of a row, one group
+        if (row < a.rows)
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) { h[i] = hv[i]; g[i] = gv[i]; r[i] = rv[i]; }
-        load(row + gridDim.x);                    // dh may be dy or dres: other rows of them
+            for (int i = 0; i < VPT; ++i)
+                if ((int)(threadIdx.x + i * blockDim.x) < nvec)
+#pragma unroll
+                    for (int q = 0; q < 3; ++q)
+                        if (q < 2 || a.dres)
+#pragma unroll
+                            for (int c = 0; c < VB; c += 16)
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, q, i)) + c),
+                                             "l"(reinterpret_cast<const char *>(src(q, row, i)) + c) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto vec = [&](int stage, int which, int64_t row, int i) {
+        Vec8<T> v;
+        v.load(STAGES ? reinterpret_cast<const T *>(slot(stage, which, i)) : src(which, row, i));
+        return v;
+    };
+    if (STAGES)
+        for (int s = 0; s < STAGES - 1; ++s) fetch(s, part + s * parts);
+    int flip = 0, stage = 0;
+    for (int64_t row = part; row < a.rows; row += parts, flip ^= 1) {
+        if (STAGES) {
+            // the slot read last round takes the row STAGES - 1 ahead (dh may be dy
+            // or dres: other rows of them)
+            fetch(stage == 0 ? STAGES - 1 : stage - 1, row + (STAGES - 1) * parts);
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES ? STAGES - 1 : 0) : "memory");
+        }
         float ss = 0.f, uh = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = min(threadIdx.x + i * blockDim.x, nvec - 1);     // past the row: zeros
+            if ((int)(threadIdx.x + i * blockDim.x) >= nvec) continue;
             float hf[8], gf[8];
-            h[i].get(hf);
-            g[i].get(gf);
-            const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * v);
-            const float4 w1 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * v + 1);
-            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            vec(stage, 0, row, i).get(hf);
+            vec(stage, 1, row, i).get(gf);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 ss = fmaf(hf[j], hf[j], ss);
-                uh = fmaf(gf[j] * w[j], hf[j], uh);
+                uh = fmaf(gf[j] * w[i][j], hf[j], uh);
             }
         }
         ss = warp_sum(ss);
         uh = warp_sum(uh);
         if (nw > 1) {                             // two buffers: one barrier per row
-            if (lane == 0) { red[flip][0][warp] = ss; red[flip][1][warp] = uh; }
+            if (lane == 0) red[flip][warp] = make_float2(ss, uh);
             __syncthreads();
             ss = 0.f;
             uh = 0.f;
-            for (int i = 0; i < nw; ++i) { ss += red[flip][0][i]; uh += red[flip][1][i]; }
+            for (int i = 0; i < nw; ++i) { ss += red[flip][i].x; uh += red[flip][i].y; }
         }
         const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.d), a.eps));
         const float m = uh * rstd * inv_d;        // mean(u * n)
@@ -245,25 +272,28 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) rmsnorm_bwd_kernel(RmsNormB
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= nvec) continue;
             float hf[8], gf[8], o[8];
-            h[i].get(hf);
-            g[i].get(gf);
-            r[i].get(o);
-            const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * v);
-            const float4 w1 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * v + 1);
-            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            vec(stage, 0, row, i).get(hf);
+            vec(stage, 1, row, i).get(gf);
+            if (a.dres) {
+                vec(stage, 2, row, i).get(o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0.f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = hf[j] * rstd;
                 dw[i][j] = fmaf(gf[j], n, dw[i][j]);
-                o[j] += rstd * (gf[j] * w[j] - n * m);
+                o[j] += rstd * (gf[j] * w[i][j] - n * m);
             }
             Vec8<T>::store(dh + v * 8, o);
         }
+        if (STAGES) stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        if (v < nvec) Vec8<float>::store(a.part + (int64_t)blockIdx.x * a.d + v * 8, dw[i]);
+        if (v < nvec) Vec8<float>::store(a.part + part * a.d + v * 8, dw[i]);
     }
 }
 
@@ -309,20 +339,50 @@ cudaError_t launch_fwd(const RmsNormArgs &a, cudaStream_t st) {
     return launch_kernel(rmsnorm_kernel<T, 4, 1024>, grid, block, 0, st, a.pdl, a);
 }
 
+template <typename T, int VPT, int MAXT, int STAGES>
+cudaError_t launch_bwd_stages(const RmsNormBwdArgs &a, int tx, int *nparts, cudaStream_t st) {
+    const int ty = tx == 32 ? 4 : 1;
+    const size_t smem = (size_t)STAGES * 3 * VPT * tx * ty * 8 * sizeof(T);
+    // as many blocks as are resident: 1024 threads and 200 KB of stages per SM
+    int per_sm = std::max(1024 / (tx * ty), 1);
+    if (STAGES) per_sm = (int)std::min<size_t>(per_sm, 200 * 1024 / smem);
+    const int blocks = std::max(1, std::min(*nparts / ty, per_sm * a.num_sms));
+    if (smem > 40 * 1024) {                       // with the static part above the default of 48 KB
+        cudaError_t e = cudaFuncSetAttribute(rmsnorm_bwd_kernel<T, VPT, MAXT, STAGES>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    *nparts = blocks * ty;
+    return launch_kernel(rmsnorm_bwd_kernel<T, VPT, MAXT, STAGES>, dim3(blocks), dim3(tx, ty), smem, st, a.pdl, a);
+}
+
+// Four rows ahead where the stages of 200 KB per SM allow, else two, else none.
+template <typename T, int VPT, int MAXT>
+cudaError_t launch_bwd_rows(const RmsNormBwdArgs &a, int tx, int *nparts, cudaStream_t st) {
+    const size_t stage = (size_t)3 * VPT * tx * 8 * sizeof(T);
+    if constexpr (MAXT <= 512)
+        if (4 * stage <= 200 * 1024) return launch_bwd_stages<T, VPT, MAXT, 4>(a, tx, nparts, st);
+    if (2 * stage <= 200 * 1024) return launch_bwd_stages<T, VPT, MAXT, 2>(a, tx, nparts, st);
+    return launch_bwd_stages<T, VPT, MAXT, 0>(a, tx, nparts, st);
+}
+
 template <typename T>
-cudaError_t launch_bwd(const RmsNormBwdArgs &a, int nparts, cudaStream_t st) {
-    int vpt, tx;
-    row_shape(a.d, &vpt, &tx);
-    const dim3 grid(nparts), block(tx);
-    if (vpt == 1) return launch_kernel(rmsnorm_bwd_kernel<T, 1, 256>, grid, block, 0, st, a.pdl, a);
-    if (vpt == 2) return launch_kernel(rmsnorm_bwd_kernel<T, 2, 256>, grid, block, 0, st, a.pdl, a);
-    if (tx <= 256) return launch_kernel(rmsnorm_bwd_kernel<T, 4, 256>, grid, block, 0, st, a.pdl, a);
-    return launch_kernel(rmsnorm_bwd_kernel<T, 4, 1024>, grid, block, 0, st, a.pdl, a);
+cudaError_t launch_bwd(const RmsNormBwdArgs &a, int *nparts, cudaStream_t st) {
+    const int nvec = a.d / 8;
+    const int vpt = nvec <= 256 ? 1 : (nvec <= 1024 ? 2 : 4);
+    const int tx = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
+    if (vpt == 1) return launch_bwd_rows<T, 1, 256>(a, tx, nparts, st);
+    if (vpt == 2) return launch_bwd_rows<T, 2, 512>(a, tx, nparts, st);
+    return launch_bwd_rows<T, 4, 1024>(a, tx, nparts, st);
 }
 
 }  // namespace
 
-int64_t rmsnorm_bwd_parts(int64_t rows) { return rows < kPartRows ? rows : kPartRows; }
+int64_t rmsnorm_bwd_parts(int64_t rows, int d) {
+    const int64_t most = (int64_t)kPartRows * (d >= 1024 ? 1 : d <= 64 ? 16 : 1024 / d);
+    const int64_t n = rows < most ? rows : most;
+    return n == 0 ? 0 : (n + 3) / 4 * 4;          // narrow rows: four at a time, the last maybe beyond
+}
 
 cudaError_t launch_rmsnorm(const RmsNormArgs &a, bool bf16, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
@@ -330,9 +390,9 @@ cudaError_t launch_rmsnorm(const RmsNormArgs &a, bool bf16, cudaStream_t st) {
 }
 
 cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs &a, bool bf16, cudaStream_t st) {
-    const int nparts = (int)rmsnorm_bwd_parts(a.rows);
+    int nparts = (int)rmsnorm_bwd_parts(a.rows, a.d);
     cudaError_t e = cudaSuccess;
-    if (nparts > 0) e = bf16 ? launch_bwd<__nv_bfloat16>(a, nparts, st) : launch_bwd<float>(a, nparts, st);
+    if (nparts > 0) e = bf16 ? launch_bwd<__nv_bfloat16>(a, &nparts, st) : launch_bwd<float>(a, &nparts, st);
     if (e != cudaSuccess) return e;
     return launch_kernel(rmsnorm_dw_kernel, dim3((unsigned)((a.d + 31) / 32)), dim3(1024), 0, st, nparts > 0 || a.pdl,
                          static_cast<const float *>(a.part), nparts, a.d, a.dweight);

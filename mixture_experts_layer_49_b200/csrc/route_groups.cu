@@ -36,10 +36,11 @@ namespace {
 constexpr int kBlockTok = 32;      // tokens per block: one row of the score sums
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+// Largest value over the warp (NaN only where every lane holds one).
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -291,7 +292,7 @@ __device__ __forceinline__ float scores(int score, int E, const float (&h)[EPT],
         float m = -INFINITY;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) m = fmaxf(m, h[j]);
-        m = warp_max(m);
+        m = redux_max(m);
         if (m == -INFINITY) m = 0.f;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) { s[j] = lane * EPT + j < E ? expf(h[j] - m) : 0.f; z += s[j]; }
@@ -335,12 +336,6 @@ __device__ __forceinline__ void get_row(const float *row, float (&v)[EPT]) {
     }
 }
 
-// Largest value over the warp (NaN only where every lane holds one).
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
 // 1 / (1 + exp(-l)): ex2 and rcp approximations, flushing below 2^-126.
 __device__ __forceinline__ float fast_sigmoid(float l) {
     float e, s;
@@ -594,19 +589,19 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     // the chosen experts' gradients to their lanes
     __syncwarp();
     put_row<EPT>(row, ds);
-    const uint32_t same = __match_any_sync(kAll, used ? e : -1 - lane);
-    if (__any_sync(kAll, (same & (same - 1u)) != 0u)) {        // an id twice: slots in order
+    if (used) row[e] = dg;
+    __syncwarp();
+    if (__any_sync(kAll, used && __float_as_uint(row[e]) != __float_as_uint(dg))) {     // an id twice: slots in order
+        if (used) row[e] = 0.f;
+        __syncwarp();
         for (int r = 0; r < a.k; ++r) {
             if (lane == r && used) row[e] += dg;
             __syncwarp();
         }
-    } else {
-        if (used) row[e] = dg;
-        __syncwarp();
     }
     get_row<EPT>(row, ds);
     if (a.alpha != 0.f) {
-        const float c = (float)((double)a.alpha * a.E / a.T / ((double)a.T * a.k));
+        const float c = a.balance;                 // alpha E / (T T k)
         float cf[EPT], dot = 0.f;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) {
@@ -673,6 +668,7 @@ cudaError_t launch_route_bwd(const RouteBwdArgs &in, cudaStream_t st) {
     RouteBwdArgs a = in;
     a.vec = vector_rows(a.logits, a.E);
     a.vec_out = vector_rows(a.dlogits, a.E);
+    a.balance = (float)((double)a.alpha * a.E / a.T / ((double)a.T * a.k));
     const dim3 grid((unsigned)((a.T + 7) / 8)), block(256);
     if (a.E <= 32) return launch_kernel(route_bwd_kernel<1>, grid, block, 0, st, a.pdl, a);
     if (a.E <= 64) return launch_kernel(route_bwd_kernel<2>, grid, block, 0, st, a.pdl, a);
