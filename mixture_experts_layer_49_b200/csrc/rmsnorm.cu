@@ -33,7 +33,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kPartRows = 592;                 // rows of partial dw sums at d >= 1024: 4 per SM
+constexpr int kPartRows = 1184;                // rows of partial dw sums at d >= 512: 8 per SM
 
 template <typename T>
 struct Vec8;                                   // eight elements of a row as loaded
@@ -180,12 +180,12 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(RmsNormArgs a) {
 
 // blockDim = (threads per row, rows at a time), rows of more than one warp one at a
 // time; part p of gridDim.x * blockDim.y takes rows p, p + parts, ...; its share of
-// dw stays in registers and ends in part[p].  The rows'
-// h, dy and dres come through shared memory by cp.async, STAGES rows ahead: each
-// thread copies and reads its own vectors, so nothing but its own wait orders
-// them, and 190 KB per SM are in flight at 16384 x 2048 bf16 (with one row held in
-// registers instead: 76 us; one row ahead in registers: 61 us; floor 41).  STAGES
-// 0: rows too wide for that, loaded as they are needed.
+// dw stays in registers and ends in part[p].  The rows' h, dy and dres come through
+// shared memory by cp.async, STAGES - 1 rows ahead: each thread copies and reads
+// its own vectors, so nothing but its own wait orders them.  16384 x 2048 bf16: 51
+// us against a floor of 41 (rows loaded as needed 76, one row ahead in registers
+// 61); 8192 x 7168 bf16 85 of 72, 8192 x 4096 fp32 85 of 82.  STAGES 0: rows too
+// wide for 200 KB of stages, loaded as they are needed.
 template <typename T, int VPT, int MAXT, int STAGES>
 __global__ void __launch_bounds__(MAXT) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
     pdl_wait_then_release();
@@ -356,12 +356,12 @@ cudaError_t launch_bwd_stages(const RmsNormBwdArgs &a, int tx, int *nparts, cuda
     return launch_kernel(rmsnorm_bwd_kernel<T, VPT, MAXT, STAGES>, dim3(blocks), dim3(tx, ty), smem, st, a.pdl, a);
 }
 
-// Four rows ahead where the stages of 200 KB per SM allow, else two, else none.
+// Three stages where two blocks of them fit an SM, else two, else none.
 template <typename T, int VPT, int MAXT>
 cudaError_t launch_bwd_rows(const RmsNormBwdArgs &a, int tx, int *nparts, cudaStream_t st) {
     const size_t stage = (size_t)3 * VPT * tx * 8 * sizeof(T);
-    if constexpr (MAXT <= 512)
-        if (4 * stage <= 200 * 1024) return launch_bwd_stages<T, VPT, MAXT, 4>(a, tx, nparts, st);
+    if constexpr (MAXT <= 256)
+        if (6 * stage <= 200 * 1024) return launch_bwd_stages<T, VPT, MAXT, 3>(a, tx, nparts, st);
     if (2 * stage <= 200 * 1024) return launch_bwd_stages<T, VPT, MAXT, 2>(a, tx, nparts, st);
     return launch_bwd_stages<T, VPT, MAXT, 0>(a, tx, nparts, st);
 }
@@ -369,17 +369,19 @@ cudaError_t launch_bwd_rows(const RmsNormBwdArgs &a, int tx, int *nparts, cudaSt
 template <typename T>
 cudaError_t launch_bwd(const RmsNormBwdArgs &a, int *nparts, cudaStream_t st) {
     const int nvec = a.d / 8;
-    const int vpt = nvec <= 256 ? 1 : (nvec <= 1024 ? 2 : 4);
+    const int vpt = nvec <= 64 ? 1 : (nvec <= 512 ? 2 : 4);
     const int tx = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
-    if (vpt == 1) return launch_bwd_rows<T, 1, 256>(a, tx, nparts, st);
-    if (vpt == 2) return launch_bwd_rows<T, 2, 512>(a, tx, nparts, st);
+    if (vpt == 1) return launch_bwd_rows<T, 1, 128>(a, tx, nparts, st);
+    if (tx <= 128) return launch_bwd_rows<T, 2, 128>(a, tx, nparts, st);
+    if (vpt == 2) return launch_bwd_rows<T, 2, 256>(a, tx, nparts, st);
+    if (tx <= 256) return launch_bwd_rows<T, 4, 256>(a, tx, nparts, st);
     return launch_bwd_rows<T, 4, 1024>(a, tx, nparts, st);
 }
 
 }  // namespace
 
 int64_t rmsnorm_bwd_parts(int64_t rows, int d) {
-    const int64_t most = (int64_t)kPartRows * (d >= 1024 ? 1 : d <= 64 ? 16 : 1024 / d);
+    const int64_t most = d >= 512 ? kPartRows : kPartRows * 512 / (d > 64 ? d : 64);
     const int64_t n = rows < most ? rows : most;
     return n == 0 ? 0 : (n + 3) / 4 * 4;          // narrow rows: four at a time, the last maybe beyond
 }
