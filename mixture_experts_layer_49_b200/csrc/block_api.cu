@@ -92,7 +92,7 @@ moe_status moe_route_select(const moe_config *cfg, const moe_route_groups *group
     a.logits = logits; a.sel_bias = sel_bias; a.idx = idx; a.gate = gate; a.psum = psum;
     a.T = cfg->T; a.E = cfg->E; a.k = cfg->top_k; a.score = cfg->score; a.renorm = cfg->renorm; a.splits = 1;
     a.n_group = groups->n_group; a.topk_group = groups->topk_group; a.group_top = groups->group_top;
-    a.gate_scale = groups->gate_scale;
+    a.gate_scale = groups->gate_scale; a.num_sms = moe::device_sms();
     return done(moe::launch_route_select(a, reinterpret_cast<cudaStream_t>(stream)), where);
 }
 

@@ -313,6 +313,7 @@ struct RouteArgs {
     int T, E, k, score, renorm, splits;
     int n_group, topk_group, group_top;
     float gate_scale;
+    int num_sms;
     int vec;                     // set by the launcher: rows load as whole vectors
     bool pdl;
 };

@@ -25,7 +25,12 @@
 // lowest id, and a lane's candidates sort with plain minima and maxima.
 //
 // The floor is the logits read once (2.8 us for 16384 x 256); the selection's
-// instructions bound it.
+// instructions bound it (8 groups of which 4 are kept, k = 8), at a register limit
+// that keeps 32 warps on an SM: 20.6 us there, 12.4 us
+// for 16384 x 128 softmax without groups, 5.5 us for 32 tokens of 256.  With 85
+// registers and 24 warps the same took 22.5, 13.9 and 5.3 us.  Rounds over 64-bit keys
+// took 50 us; the doubtful tokens in a pass of their own after the others 23 (14.4
+// against 7.5 for 1000 tokens).
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -61,9 +66,6 @@ __device__ __forceinline__ uint64_t image(double f) {
     const uint64_t u = (uint64_t)__double_as_longlong(f);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
-// fp64 keys decide; only fp32 keys are asked how close they are.
-template <typename F> __device__ __forceinline__ constexpr bool close_matters() { return sizeof(F) == 4; }
-
 template <typename F>
 __device__ __forceinline__ F low() { return (F)(-INFINITY); }
 
@@ -172,7 +174,7 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&k
         }
     }
     *close = false;
-    if (close_matters<F>()) {                      // a NaN bound (infinite scores) compares false: not close
+    if constexpr (sizeof(F) == 4) {                // fp64 keys decide; a NaN bound (infinite scores) compares false: not close
         uint32_t lo = ordered((float)wk), hi = ordered((float)bd);
         lo = __reduce_min_sync(kAll, lo);
         hi = __reduce_max_sync(kAll, hi);
@@ -202,34 +204,33 @@ __device__ __forceinline__ void lane_sort(uint32_t (&v)[EPT]) {
 }
 
 // Logits of token t, offset included: `splits` partial planes added in order.
-template <int EPT>
+// FULL: E = 32 EPT and rows of whole aligned vectors, so no lane is short.
+template <int EPT, bool FULL>
 __device__ __forceinline__ void load_logits(const RouteArgs &a, int t, float (&h)[EPT]) {
     const int lane = threadIdx.x & 31;
     const float *p = a.logits + (size_t)t * a.E + lane * EPT;
     const size_t plane = (size_t)a.T * a.E;
-    if (a.vec) {                                   // E % EPT == 0 and aligned: whole vectors
+    if (FULL || a.vec) {                           // E % EPT == 0 and aligned: whole vectors
         constexpr int W = EPT < 4 ? EPT : 4;
+        if (!FULL)
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) h[j] = -INFINITY;
-        if (lane * EPT < a.E) {
-            for (int s = 0; s < a.splits; ++s) {
+            for (int j = 0; j < EPT; ++j) h[j] = -INFINITY;
+        if (FULL || lane * EPT < a.E) {
 #pragma unroll
-                for (int q = 0; q < EPT; q += W) {
-                    float f[4];
-                    if constexpr (W == 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(p + q);
-                        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-                    } else if constexpr (W == 2) {
-                        const float2 v = *reinterpret_cast<const float2 *>(p + q);
-                        f[0] = v.x; f[1] = v.y;
-                    } else {
-                        f[0] = p[q];
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j) h[q + j] = s == 0 ? f[j] : h[q + j] + f[j];
+            for (int q = 0; q < EPT; q += W) {
+                if constexpr (W == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p + q);
+                    h[q] = v.x; h[q + 1] = v.y; h[q + 2] = v.z; h[q + 3] = v.w;
+                } else if constexpr (W == 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(p + q);
+                    h[q] = v.x; h[q + 1] = v.y;
+                } else {
+                    h[q] = p[q];
                 }
-                p += plane;
             }
+            for (int s = 1; s < a.splits; ++s)
+#pragma unroll
+                for (int j = 0; j < EPT; ++j) h[j] += p[s * plane + j];
         }
     } else {
 #pragma unroll
@@ -250,7 +251,7 @@ template <int EPT>
 __device__ __noinline__ int select_exact(const RouteArgs &a, int t) {
     const int lane = threadIdx.x & 31;
     float h[EPT];
-    load_logits<EPT>(a, t, h);
+    load_logits<EPT, false>(a, t, h);
     double key[EPT];
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
@@ -343,16 +344,65 @@ __device__ __forceinline__ float fast_sigmoid(float l) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
     return s;
 }
-// The distance in a candidate's word.
+// The 64-bit key of a logit.
+__device__ __forceinline__ double key64(const RouteArgs &a, float l, int e) {
+    const double k = a.score == MOE_SCORE_SOFTMAX ? (double)l : 1.0 / (1.0 + exp(-(double)l));
+    return a.sel_bias ? k + (double)a.sel_bias[e] : k;
+}
+__device__ __forceinline__ float one_logit(const RouteArgs &a, int t, int e) {
+    const float *p = a.logits + (size_t)t * a.E + e;
+    float h = p[0];
+    for (int s = 1; s < a.splits; ++s) h += p[(size_t)s * a.T * a.E];
+    return h;
+}
+
+// Error bounds.  A sigmoid key: ex2 of a rounded product is off by (2 + 1.2 |l|)
+// ulp, which moves s by s (1 - s) of that, at most 1.3 * 2^-24; the sum rounds by
+// 2^-24, rcp by an ulp: together below 4.3 * 2^-24 (s <= 1); the sum with the bias
+// by 2^-24 of it.  A softmax key: the latter alone.  Two distances from the best
+// key mx: besides their keys, cut off at 2^-15 of them and one rounding (and 2^-140,
+// what the cut takes off a subnormal one).
+struct Bounds {
+    float abs, rel;                                // of a key
+    __device__ __forceinline__ explicit Bounds(const RouteArgs &a)
+        : abs(a.score == MOE_SCORE_SOFTMAX ? 0.f : 0x1p-21f),
+          rel(a.score == MOE_SCORE_SOFTMAX && !a.sel_bias ? 0.f : 0x1p-23f) {}
+    __device__ __forceinline__ float two(float mx) const { return 2.f * abs + 2.f * rel * fabsf(mx) + 0x1p-140f; }
+    __device__ __forceinline__ float two_rel() const { return 0x1.2p-14f + 2.f * rel; }
+};
+
+// A lane's candidates: 24 bits of the distance from the best key (a NaN key's is
+// NaN, above all others), then the id.
+template <int EPT, bool FULL>
+__device__ __forceinline__ void candidates(const RouteArgs &a, const float (&key)[EPT], float mx, uint32_t (&v)[EPT]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        const uint32_t e = lane * EPT + j;
+        v[j] = FULL || e < (uint32_t)a.E ? (__float_as_uint(mx - key[j]) & 0x7fffff00u) | e : kAll;
+    }
+}
 __device__ __forceinline__ float distance(uint32_t word) { return __uint_as_float(word & 0x7fffff00u); }
 
-// The topk_group best groups where a lane's candidates (sorted, best first)
-// belong to one group and a group is `lanes` (a power of two) neighbouring
-// lanes: the sum of a group's best distances, its id in the low 8 bits, and one
-// redux per kept group.  Whether this lane's group is kept; *close as above.
+// Takes the best candidate over the warp out of its lane's sorted list.
 template <int EPT>
-__device__ __forceinline__ bool kept_lane(const RouteArgs &a, int lanes, const uint32_t (&v)[EPT], float tol0, float tol_rel,
-                                          bool *close) {
+__device__ __forceinline__ uint32_t take_best(uint32_t (&v)[EPT]) {
+    const uint32_t top = __reduce_min_sync(kAll, v[0]);
+    const bool win = v[0] == top;
+#pragma unroll
+    for (int j = 0; j + 1 < EPT; ++j) v[j] = win ? v[j + 1] : v[j];
+    v[EPT - 1] = win ? kAll : v[EPT - 1];
+    return top;
+}
+
+// The topk_group best groups where a lane's candidates (sorted, best first) belong
+// to one group and a group is `lanes` (a power of two) neighbouring lanes: the sum
+// of a group's best distances, its id in the low 8 bits, and one redux per kept
+// group.  Whether this lane's group is kept; *close: whether the border is within
+// the bounds.
+template <int EPT>
+__device__ __forceinline__ bool kept_lane(const RouteArgs &a, int lanes, const uint32_t (&v)[EPT], float two,
+                                          float two_rel, bool *close) {
     const int lane = threadIdx.x & 31;
     uint32_t t1 = v[0], t2 = EPT > 1 ? v[EPT > 1 ? 1 : 0] : kAll;
     for (int o = 1; o < lanes; o <<= 1) {
@@ -372,21 +422,16 @@ __device__ __forceinline__ bool kept_lane(const RouteArgs &a, int lanes, const u
     }
     const float last = distance(top), next = distance(__reduce_min_sync(kAll, word));
     // two keys a score; each distance and the sum cut off at 2^-15
-    *close = next - last < 2.f * tol0 + 2.f * tol_rel * next;
+    *close = next - last < 2.f * two + 2.f * two_rel * next;
     return kept;
 }
 
 // The best a.k of n <= 31 candidates (lane r < n holds one) by their 64-bit keys:
 // lane r's chosen id of rank r.
-__device__ __noinline__ int rank_exact(const RouteArgs &a, int t, uint32_t mine, int n) {
+__device__ __forceinline__ int rank_exact(const RouteArgs &a, int t, uint32_t mine, int n) {
     const int lane = threadIdx.x & 31;
     const int id = lane < n ? (int)(mine & 255u) : 0;
-    const float *p = a.logits + (size_t)t * a.E + id;
-    float h = p[0];
-    for (int s = 1; s < a.splits; ++s) h += p[(size_t)s * a.T * a.E];
-    double key = a.score == MOE_SCORE_SOFTMAX ? (double)h : 1.0 / (1.0 + exp(-(double)h));
-    if (a.sel_bias) key += (double)a.sel_bias[id];
-    const uint64_t im = image(key);
+    const uint64_t im = image(key64(a, one_logit(a, t, id), id));
     int rank = 0;
     for (int q = 0; q < n; ++q) {
         const uint64_t o = __shfl_sync(kAll, im, q);
@@ -402,41 +447,57 @@ __device__ __noinline__ int rank_exact(const RouteArgs &a, int t, uint32_t mine,
     return lane < a.k ? chosen : 0;
 }
 
-template <int EPT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __grid_constant__ RouteArgs a) {
+// Lanes per group where no lane's experts span two groups and the lanes of a group
+// are a power of two, else 0.
+template <int EPT>
+__device__ __forceinline__ int lanes_per_group(const RouteArgs &a) {
+    const int size = a.E / a.n_group;
+    return size % EPT == 0 && ((size / EPT) & (size / EPT - 1)) == 0 ? size / EPT : 0;
+}
+
+// Gates of the chosen ids (lane r < k holds one) from the scores in `row`.
+__device__ __forceinline__ void write_choice(const RouteArgs &a, int t, int my_id, const float *row) {
+    const int lane = threadIdx.x & 31;
+    const float g = row[my_id];
+    float f = g * a.gate_scale;
+    if (a.score != MOE_SCORE_SOFTMAX || a.renorm) {
+        const float sum = warp_sum(lane < a.k ? g : 0.f);
+        f = sum == 0.f ? 0.f : g / sum * a.gate_scale;      // no scores left: gates of 0
+    }
+    if (lane < a.k) {
+        a.idx[(size_t)t * a.k + lane] = my_id;
+        a.gate[(size_t)t * a.k + lane] = f;
+    }
+}
+
+// ALIGNED: every token may use every group, or lanes_per_group is not 0.
+template <int EPT, int WARPS, bool FULL, bool ALIGNED>
+__global__ void __launch_bounds__(WARPS * 32, 1024 / (WARPS * 32)) route_select_kernel(const __grid_constant__ RouteArgs a) {
     pdl_wait_then_release();
     __shared__ __align__(16) float part[WARPS][EPT * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-    const int size = a.E / a.n_group;
-    const int lanes = size % EPT == 0 && ((size / EPT) & (size / EPT - 1)) == 0 ? size / EPT : 0;   // 0: groups end inside lanes
+    const int lanes = ALIGNED ? lanes_per_group<EPT>(a) : 0;
+    const Bounds bounds(a);
+    const float two_rel = bounds.two_rel();
     float sb[EPT], share[EPT];
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
-        sb[j] = (a.sel_bias && lane * EPT + j < a.E) ? __ldg(a.sel_bias + lane * EPT + j) : 0.f;
+        sb[j] = (a.sel_bias && (FULL || lane * EPT + j < a.E)) ? __ldg(a.sel_bias + lane * EPT + j) : 0.f;
         share[j] = 0.f;
     }
-    // Error of a key.  Sigmoid: ex2 of a rounded product is off by (2 + 1.2 |l|) ulp,
-    // which moves s by s (1 - s) of that, at most 1.3 * 2^-24; the sum rounds by
-    // 2^-24, rcp by an ulp: together below 4.3 * 2^-24 (s <= 1); the sum with the
-    // bias by 2^-24 of it.  Softmax: the latter alone.
-    const float err_abs = softmax ? 0.f : 0x1p-21f;
-    const float err_rel = (softmax && !a.sel_bias) ? 0.f : 0x1p-23f;
-    // Two distances: cut off at 2^-15 of them and one rounding, besides the keys.
-    const float tol_rel = 0x1.2p-14f + 2.f * err_rel;
     for (int i = 0; i < kBlockTok / WARPS; ++i) {
         const int t = blockIdx.x * kBlockTok + i * WARPS + warp;
         if (t >= a.T) break;                       // uniform over the warp
         float h[EPT], s[EPT], key[EPT];
-        load_logits<EPT>(a, t, h);
+        load_logits<EPT, FULL>(a, t, h);
         if (a.logits_out) {
 #pragma unroll
             for (int j = 0; j < EPT; ++j)
-                if (lane * EPT + j < a.E) a.logits_out[(size_t)t * a.E + lane * EPT + j] = h[j];
+                if (FULL || lane * EPT + j < a.E) a.logits_out[(size_t)t * a.E + lane * EPT + j] = h[j];
         }
-        float inv, mx;
         if (softmax) {
-            inv = scores<EPT>(a.score, a.E, h, s);
+            const float inv = scores<EPT>(a.score, a.E, h, s);
 #pragma unroll
             for (int j = 0; j < EPT; ++j) {
                 s[j] *= inv;
@@ -448,73 +509,57 @@ __global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __gri
 #pragma unroll
             for (int j = 0; j < EPT; ++j) { s[j] = fast_sigmoid(h[j]); z += s[j]; }      // absent experts: 0
             z = warp_sum(z);
-            inv = z == 0.f ? 0.f : 1.f / z;
+            const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
             for (int j = 0; j < EPT; ++j) {
                 share[j] = fmaf(s[j], inv, share[j]);
-                key[j] = lane * EPT + j < a.E ? s[j] + sb[j] : -INFINITY;
+                key[j] = FULL || lane * EPT + j < a.E ? s[j] + sb[j] : -INFINITY;
             }
         }
-        mx = key[0];
+        put_row<EPT>(part[warp], s);
+        float mx = key[0];
 #pragma unroll
         for (int j = 1; j < EPT; ++j) mx = fmaxf(mx, key[j]);
         mx = redux_max(mx);
         bool close = !(fabsf(mx) < INFINITY);      // an infinite best key: distances say nothing
-        // candidates: 24 bits of the distance from the best key (a NaN key's is NaN,
-        // above all others), then the id
         uint32_t v[EPT];
-#pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            const uint32_t e = lane * EPT + j;
-            v[j] = e < (uint32_t)a.E ? (__float_as_uint(mx - key[j]) & 0x7fffff00u) | e : kAll;
-        }
-        // (2^-140: what the cut takes off a subnormal distance)
-        const float tol0 = 2.f * err_abs + 2.f * err_rel * fabsf(mx) + 0x1p-140f;
+        candidates<EPT, FULL>(a, key, mx, v);
+        const float two = bounds.two(mx);
+        // two roundings more per score than per key, both within twice rel
+        const float score_rel = softmax ? 0x1p-22f : 2.f * bounds.rel;
         bool c = false;
-        if (a.topk_group == a.n_group) {
-            lane_sort<EPT>(v);
-        } else if (lanes) {
-            lane_sort<EPT>(v);
-            bool kept = kept_lane<EPT>(a, lanes, v, tol0, tol_rel, &c);
-            if (c)                                 // too close for cut-off distances: whole fp32 keys
-                kept = kept_experts<EPT, float>(a, key, err_abs, softmax ? 0x1p-22f : 2.f * err_rel, &c) != 0u;
-#pragma unroll
-            for (int j = 0; j < EPT; ++j) v[j] = kept ? v[j] : kAll;
-        } else {
-            // two roundings more per score than per key, both within rel
-            const uint32_t mask = kept_experts<EPT, float>(a, key, err_abs, softmax ? 0x1p-22f : 2.f * err_rel, &c);
+        if (!ALIGNED) {
+            const uint32_t mask = kept_experts<EPT, float>(a, key, bounds.abs, score_rel, &c);
 #pragma unroll
             for (int j = 0; j < EPT; ++j) v[j] = mask >> j & 1u ? v[j] : kAll;
-            lane_sort<EPT>(v);
         }
-        // k rounds: the best candidate over the warp leaves its lane's list; lane r
-        // keeps the winner of round r, lane k (or `next`) the best one left out
-        uint32_t mine = kAll;
-        for (int r = 0; r < a.k; ++r) {
-            const uint32_t top = __reduce_min_sync(kAll, v[0]);
-            const bool win = v[0] == top;
+        lane_sort<EPT>(v);
+        if (ALIGNED && a.topk_group < a.n_group) {
+            bool kept = kept_lane<EPT>(a, lanes, v, two, two_rel, &c);
+            if (c)                                 // too close for cut-off distances: whole fp32 keys
+                kept = kept_experts<EPT, float>(a, key, bounds.abs, score_rel, &c) != 0u;
 #pragma unroll
-            for (int j = 0; j + 1 < EPT; ++j) v[j] = win ? v[j + 1] : v[j];
-            v[EPT - 1] = win ? kAll : v[EPT - 1];
+            for (int j = 0; j < EPT; ++j) v[j] = kept ? v[j] : kAll;
+        }
+        uint32_t mine = kAll;                      // lane r: the winner of round r
+        for (int r = 0; r < a.k; ++r) {
+            const uint32_t top = take_best<EPT>(v);
             mine = lane == r ? top : mine;
         }
         uint32_t next = __reduce_min_sync(kAll, v[0]);
         uint32_t after = __shfl_down_sync(kAll, mine, 1);
         if (lane == a.k - 1) after = next;
         // an infinite or NaN distance compares false: not close, ids decide
-        const bool tight = lane < a.k && after != kAll && distance(after) - distance(mine) < tol0 + tol_rel * distance(after);
+        const bool tight = lane < a.k && after != kAll && distance(after) - distance(mine) < two + two_rel * distance(after);
         int my_id = lane < a.k ? (int)(mine & 255u) : 0;
         close = close || c;
         if (!close && __any_sync(kAll, tight)) {
-            // the chosen and whatever lies within the bound behind them, one to a
+            // the chosen and whatever lies within the bounds behind them, one to a
             // lane, ranked by their 64-bit keys
             const float limit = distance(__shfl_sync(kAll, mine, a.k - 1));
             int n = a.k;
-            while (n < 32 && next != kAll && distance(next) - limit < tol0 + tol_rel * distance(next)) {
-                const bool win = v[0] == next;
-#pragma unroll
-                for (int j = 0; j + 1 < EPT; ++j) v[j] = win ? v[j + 1] : v[j];
-                v[EPT - 1] = win ? kAll : v[EPT - 1];
+            while (n < 32 && next != kAll && distance(next) - limit < two + two_rel * distance(next)) {
+                take_best<EPT>(v);
                 mine = lane == n ? next : mine;
                 ++n;
                 next = __reduce_min_sync(kAll, v[0]);
@@ -523,19 +568,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2) route_select_kernel(const __gri
             else my_id = rank_exact(a, t, mine, n);
         }
         if (close) my_id = select_exact<EPT>(a, t);
-        // the chosen scores by id, through the warp's row of `part`
-        put_row<EPT>(part[warp], s);
-        const float g = part[warp][my_id];
+        write_choice(a, t, my_id, part[warp]);
         __syncwarp();
-        float f = g * a.gate_scale;
-        if (!softmax || a.renorm) {
-            const float sum = warp_sum(lane < a.k ? g : 0.f);
-            f = sum == 0.f ? 0.f : g / sum * a.gate_scale;   // no scores left: gates of 0
-        }
-        if (lane < a.k) {
-            a.idx[(size_t)t * a.k + lane] = my_id;
-            a.gate[(size_t)t * a.k + lane] = f;
-        }
     }
     if (a.psum == nullptr) return;
     put_row<EPT>(part[warp], share);
@@ -563,7 +597,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     RouteArgs ra{};
     ra.logits = a.logits; ra.T = a.T; ra.E = a.E; ra.splits = 1; ra.vec = a.vec;
     float h[EPT], s[EPT], ds[EPT];
-    load_logits<EPT>(ra, t, h);
+    load_logits<EPT, false>(ra, t, h);
     const float inv = scores<EPT>(a.score, a.E, h, s);
     int e = -1;
     float dg = 0.f;
@@ -641,7 +675,26 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     }
 }
 
-constexpr int kSelWarps = 16;
+constexpr int kSelWarps = 8;
+
+template <int EPT, int W>
+cudaError_t launch_select_warps(const RouteArgs &a, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.T + kBlockTok - 1) / kBlockTok)), block(W * 32);
+    const int size = a.E / a.n_group, lanes = size % EPT == 0 ? size / EPT : 0;
+    const bool aligned = a.topk_group == a.n_group || (lanes > 0 && (lanes & (lanes - 1)) == 0);
+    if (!aligned) return launch_kernel(route_select_kernel<EPT, W, false, false>, grid, block, 0, st, a.pdl, a);
+    if (a.vec && a.E == 32 * EPT) return launch_kernel(route_select_kernel<EPT, W, true, true>, grid, block, 0, st, a.pdl, a);
+    return launch_kernel(route_select_kernel<EPT, W, false, true>, grid, block, 0, st, a.pdl, a);
+}
+
+// Where all blocks run at once a token has a warp of its own (T = 256: 7.4 us against
+// 9.5 with four to a warp, 4000: 7.9 against 10.0); beyond that four tokens share a
+// warp's start and its part of the score sums (8000: 12.5 us against 13.5).
+template <int EPT>
+cudaError_t launch_select(const RouteArgs &a, cudaStream_t st) {
+    if ((a.T + kBlockTok - 1) / kBlockTok <= a.num_sms) return launch_select_warps<EPT, 32>(a, st);
+    return launch_select_warps<EPT, kSelWarps>(a, st);
+}
 
 // A row of E fp32 values splits into whole aligned vectors of the lanes.
 int vector_rows(const void *p, int E) {
@@ -656,11 +709,10 @@ cudaError_t launch_route_select(const RouteArgs &in, cudaStream_t st) {
     if (in.T == 0) return cudaSuccess;
     RouteArgs a = in;
     a.vec = vector_rows(a.logits, a.E);
-    const dim3 grid((unsigned)((a.T + kBlockTok - 1) / kBlockTok)), block(kSelWarps * 32);
-    if (a.E <= 32) return launch_kernel(route_select_kernel<1, kSelWarps>, grid, block, 0, st, a.pdl, a);
-    if (a.E <= 64) return launch_kernel(route_select_kernel<2, kSelWarps>, grid, block, 0, st, a.pdl, a);
-    if (a.E <= 128) return launch_kernel(route_select_kernel<4, kSelWarps>, grid, block, 0, st, a.pdl, a);
-    return launch_kernel(route_select_kernel<8, kSelWarps>, grid, block, 0, st, a.pdl, a);
+    if (a.E <= 32) return launch_select<1>(a, st);
+    if (a.E <= 64) return launch_select<2>(a, st);
+    if (a.E <= 128) return launch_select<4>(a, st);
+    return launch_select<8>(a, st);
 }
 
 cudaError_t launch_route_bwd(const RouteBwdArgs &in, cudaStream_t st) {

@@ -368,7 +368,7 @@ cudaError_t launch_router_any(const RouterArgs &a, bool bf16, const moe_route_gr
     r.idx = a.idx; r.gate = a.gate; r.psum = a.psum;
     r.T = a.T; r.E = a.E; r.k = a.k; r.score = a.score; r.renorm = a.renorm;
     r.n_group = groups->n_group; r.topk_group = groups->topk_group; r.group_top = groups->group_top;
-    r.gate_scale = groups->gate_scale;
+    r.gate_scale = groups->gate_scale; r.num_sms = a.num_sms;
     r.pdl = true;
     return launch_route_select(r, st);
 }
