@@ -11,20 +11,29 @@
 // sums never leave fp32 and the partial products of 128 terms are the longest
 // chain that the tensor core rounds.
 //
-// One persistent CTA per SM, tile 128 rows x 256 accumulator columns (SwiGLU:
-// 128 gate and 128 up columns), 320 threads:
-//   warp 0      TMA producer, 4 stages of A 128 x 128 and B 256 x 128 bytes
-//   warp 1      TMEM allocator and tcgen05.mma issuer
-//   warps 2..9  the scaled sums (two warps per TMEM lane quadrant, 128 columns
-//               each: 128 fp32 registers a thread) and the epilogue
+// Persistent CTAs of 384 threads, one to an SM, alone (128 rows x 256
+// accumulator columns, 4 stages of 48 KiB) or in pairs (256 x 256, 6 stages of
+// 32 KiB a CTA); SwiGLU's columns are 128 of the gate and 128 of the up product:
+//   warp 0       TMA producer
+//   warps 1, 2   TMEM allocator (1) and tcgen05.mma issuers of the even and odd
+//                K blocks
+//   warp 3       idle: it fills the first warpgroup, which gives its registers away
+//   warps 4..11  the scaled sums (two warps per TMEM lane quadrant, 128 columns
+//                each: 128 fp32 registers a thread) and the epilogue
 // Epilogues: SwiGLU and GELU quantize the hidden row's block of 128 straight
 // from the fp32 sums (one rounding), so the second product reads codes and
 // scales and no pass over H runs in between; the down projection adds the bias,
 // applies the gate and rounds once to bf16.
 //
-// Per K block the tensor core needs 512 cycles (128 x 256 x 128 products at
-// 8192 per cycle); the sums need 32768 TMEM words (512 bytes a cycle: 256
-// cycles) and as many fused multiply-adds (two per lane and cycle: 128 cycles).
+// Per K block and CTA the tensor core needs 512 cycles (128 x 256 x 128 products
+// at 8192 per cycle) and a pair's loop takes 835 (8192 x 28672 x 4096: 905 us
+// for the first runs, then the power limit holds the clock near 1.4 GHz and it
+// takes 1070).  The scaled sums make the difference: without the multiply-adds
+// the same loop runs at 600 cycles, without the TMEM loads too at 520, without
+// the copies still at 860.  None of these went below 825: half accumulators of
+// 128 columns with barriers of their own, loads of 32 columns beside the
+// multiply-adds of the last 32, packed f32x2 multiply-adds.  A library product of
+// these sizes with one scale per tensor, so without the sums, takes 757 us.
 //
 // Every mbarrier wait is bounded as in the other tensor-core kernels; a wait
 // that runs out records MOE_ERR_TIMEOUT, and the CTA lets its copies and
@@ -463,9 +472,10 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t tmem_base = s.tmem_base;
 
     // registers: launched with 168 a thread (3 x 128 x 168), redistributed as
-    // 128 x 88 + 256 x 208, the same total
+    // 128 x 56 + 256 x 224, the same total (88 and 208 left the sums 64 bytes of
+    // spills: 860 instead of 835 cycles a K block)
     if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       if (warp == 0) {
         // ================= TMA producer
         if (lane == 0) {
@@ -539,7 +549,7 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         __syncwarp();
       }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ================= scaled sums and epilogue: warps 4..11
         sums_warps<MODE, false>(s, p, tmem_base, base + (uint32_t)kStgOff, total, blockIdx.x, gridDim.x, 0);
     }
@@ -617,7 +627,7 @@ fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
 
     // registers as in the 1-CTA kernel
     if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       if (warp == 0) {
         // ================= TMA producer (both CTAs)
         if (lane == 0) {
@@ -684,7 +694,7 @@ fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         }
       }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         sums_warps<MODE, true>(s, p, tmem_base, base + (uint32_t)kPairStgOff, total, pair, npairs, (int)rank);
     }
 
