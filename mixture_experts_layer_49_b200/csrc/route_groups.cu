@@ -27,7 +27,7 @@
 // The floor is the logits read once (2.8 us for 16384 x 256); the selection's
 // instructions bound it (8 groups of which 4 are kept, k = 8), at a register limit
 // that keeps 32 warps on an SM: 20.6 us there, 12.4 us
-// for 16384 x 128 softmax without groups, 5.5 us for 32 tokens of 256.  With 85
+// for 16384 x 128 softmax without groups, 5.5 us for 16 tokens of 256.  With 85
 // registers and 24 warps the same took 22.5, 13.9 and 5.3 us.  Rounds over 64-bit keys
 // took 50 us; the doubtful tokens in a pass of their own after the others 23 (14.4
 // against 7.5 for 1000 tokens).
