@@ -65,6 +65,25 @@ def test_selection(cuda_device, E, k, groups, score, renorm, bias):
         check(logits, b, k, groups, score, renorm)
 
 
+@pytest.mark.parametrize("score,renorm,bias", [("sigmoid", 1, True), ("softmax", 0, False)])
+@pytest.mark.parametrize("E,k,groups", CASES)
+def test_many_tokens(cuda_device, E, k, groups, score, renorm, bias):
+    """More blocks than SMs take four tokens to a warp: the same choices as in
+    calls of few tokens, gates and sums each within TOL of the exact ones."""
+    g = torch.Generator(device=cuda_device).manual_seed(E * 100 + k + 1)
+    sms = torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    T = 32 * (sms + 9) + 5
+    logits = 2.0 * torch.randn((T, E), generator=g, device=cuda_device)
+    b = 0.3 * torch.randn(E, generator=g, device=cuda_device) if bias else None
+    idx, gate, psum = run(logits, b, k, groups, score, renorm)
+    for t in range(0, T, 1024):
+        i, w, p = run(logits[t:t + 1024], b, k, groups, score, renorm)
+        assert torch.equal(idx[t:t + 1024], i)
+        assert ((gate[t:t + 1024] - w).abs() <= 2 * TOL * w.abs() + 2e-37).all()
+        q = psum[t // 32:t // 32 + p.shape[0]]
+        assert ((q - p).abs() <= 2 * TOL * p.abs() + 2e-37).all()
+
+
 def test_unaligned_rows(cuda_device):
     g = torch.Generator(device=cuda_device).manual_seed(4)
     raw = torch.randn(64 * 256 + 3, generator=g, device=cuda_device)
