@@ -132,6 +132,18 @@ def test_grouped_ffn(cuda_device, T, d, E, F, k, act, S, counts):
     check(cfg, counts, w, r)
 
 
+# enough tiles for CTA pairs in one of the products, with last blocks of 1, 127, 128, 129
+# and more rows, experts without rows, the shared expert and biases
+@pytest.mark.parametrize("T,d,E,F,k,act,S,counts", [
+    (4600, 144, 5, 2064, 2, "swiglu", 272, [4000, 129, 0, 4815, 256]),
+    (15000, 1040, 5, 144, 2, "swiglu", 144, [29000, 1, 127, 700, 0]),
+    (17400, 144, 4, 2064, 1, "gelu", 0, [17000, 130, 14, 256]),
+    (31000, 1040, 4, 144, 1, "gelu", 0, [29900, 0, 900, 128]),
+])
+def test_grouped_ffn_of_many_rows(cuda_device, T, d, E, F, k, act, S, counts):
+    test_grouped_ffn(cuda_device, T, d, E, F, k, act, S, counts)
+
+
 def test_scales_of_every_block_count(cuda_device):
     """Scales spread over 2^-20 .. 2^20: a block scaled by a neighbour's scale would
     be far off."""
