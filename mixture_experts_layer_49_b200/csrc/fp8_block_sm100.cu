@@ -283,6 +283,7 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
             ok = mbar_wait(xch, xphase, p.timeout_ns) ? 1 : 0;
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+        __syncwarp();                                      // lane 0's wait orders memory for the other lanes by this
         amax = fmaxf(amax, amax_buf[c.half ^ 1][r_in_tile]);
     } else {
         if (c.bias) {

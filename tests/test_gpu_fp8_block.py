@@ -334,3 +334,28 @@ def test_group_limited_training(cuda_device):
     for n in ("dW1", "dWu", "dW2", "dx", "dWr"):
         a, b = res[1.0][n].double(), res[2.0][n].double()
         assert (b - 2 * a).norm() <= 2.0 ** -16 * b.norm() + 1e-30, n
+
+
+# T, d, E, F, k, S: one CTA a tile, CTA pairs in the first product, in both with the
+# shared expert, and the form for one and two tokens
+@pytest.mark.parametrize("T,d,E,F,k,act,S", [
+    (2000, 1040, 16, 400, 2, "swiglu", 0), (9000, 144, 8, 2064, 2, "swiglu", 272), (15000, 1040, 5, 272, 2, "swiglu", 144),
+    (2000, 1040, 16, 400, 1, "gelu", 0), (2, 2048, 64, 768, 8, "swiglu", 768),
+])
+def test_repeated_calls_give_the_same_bits(cuda_device, T, d, E, F, k, act, S):
+    """The two warps that share a hidden row's block exchange its maximum: a maximum
+    read too early would change codes from call to call."""
+    wl = syn.Workload("block", T=T, d_model=d, E=E, d_ff=F, top_k=k, act=act, d_ff_shared=S)
+    cfg = nat.config_from_workload(wl)
+    sld = nat.fp8_block_sld(cfg)
+    w = syn.generate_fp8_block_experts(wl, sld, cuda_device, seed=6)
+    counts = torch.bincount(torch.randint(0, E, (T * k,), generator=torch.Generator().manual_seed(T)), minlength=E).tolist()
+    r = grouped(cfg, None, counts, w, sld, cuda_device, T, act == "gelu")
+    first = r["y"].clone()
+    assert torch.isfinite(first).all()
+    for _ in range(20):
+        r["y"].fill_(776.0)
+        nat.moe_grouped_ffn_fp8_block(cfg, r["x8"], r["xs"], r["offsets"], r["gate"], r["ex"], w.get("b1"), w.get("b2"),
+                                      r["xt8"], r["xts"], r["y"], r["ws"])
+        assert torch.equal(r["y"], first)
+    assert nat.moe_get_device_status(r["ws"]) == nat.MOE_OK
