@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     put_row<EPT>(row, ds);
     if (used) row[e] = dg;
     __syncwarp();
-    if (__any_sync(kAll, used && __float_as_uint(row[e]) != __float_as_uint(dg))) {     // an id twice: slots in order
+    const unsigned same = __match_any_sync(kAll, used ? e : -1 - lane);
+    if (__any_sync(kAll, (same & (same - 1u)) != 0u)) {        // an id twice: slots in order
         if (used) row[e] = 0.f;
         __syncwarp();
         for (int r = 0; r < a.k; ++r) {

@@ -251,3 +251,25 @@ def test_router_stage_agrees_with_the_selection_of_its_logits(cuda_device):
         want = ref.select(logits.cpu(), sb.cpu(), 4, 1, 1, 1, "sigmoid")
         assert torch.equal(i2.cpu(), want)
         assert nat.moe_get_device_status(ws) == nat.MOE_OK
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", 1), ("softmax", 1), ("softmax", 0)])
+@pytest.mark.parametrize("equal", [True, False])
+def test_gradient_of_an_id_that_stands_twice(cuda_device, equal, score, renorm):
+    """The slots of one id add up, whether their gate gradients are equal or not.
+    dgate and logits are bounded by 1, k = 6: every term is at most 2.5 and a
+    row adds fewer than 32 of them with 2^-15 each (the module's tolerance)."""
+    T, E, k, scale, alpha = 40, 64, 6, 2.5, 0.5
+    g = torch.Generator(device=cuda_device).manual_seed(21)
+    logits = 2.0 * torch.rand((T, E), generator=g, device=cuda_device) - 1.0
+    idx = torch.randint(0, 9, (T, k), generator=g, device=cuda_device).to(torch.int32)
+    idx[0] = 5                                                  # one expert in every slot
+    dgate = 2.0 * torch.rand((T, E if equal else k), generator=g, device=cuda_device) - 1.0
+    if equal:                                                   # one gradient per expert
+        dgate = dgate.gather(1, idx.long()).contiguous()
+    counts = torch.bincount(idx.flatten().long(), minlength=E).to(torch.int32)
+    d = torch.empty((T, E), device=cuda_device)
+    nat.moe_route_backward(config(T, E, k, score, renorm), nat.route_groups(1, 1, 1, scale), logits, idx, dgate, counts,
+                           alpha, d)
+    want = ref.route_backward(logits.cpu(), idx.cpu(), dgate.cpu(), counts.cpu(), alpha, score, renorm, scale)
+    assert ((d.cpu().double() - want).abs() <= 32 * 2.5 * 2.0 ** -15).all()
