@@ -26,7 +26,7 @@
 //
 // The floor is the logits read once (2.8 us for 16384 x 256); the selection's
 // instructions bound it (8 groups of which 4 are kept, k = 8), at a register limit
-// that keeps 32 warps on an SM: 20.6 us there, 12.4 us
+// that keeps 32 warps on an SM: 22.5 us there, 12.4 us
 // for 16384 x 128 softmax without groups, 5.5 us for 16 tokens of 256.  With 85
 // registers and 24 warps the same took 22.5, 13.9 and 5.3 us.  Rounds over 64-bit keys
 // took 50 us; the doubtful tokens in a pass of their own after the others 23 (14.4
@@ -283,6 +283,10 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int t) {
     return my_id;
 }
 
+// 1 / (1 + exp(-l)) within three units of 2^-23; 0 below -88.72, where exp(-l)
+// passes the largest fp32 number.
+__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+
 // Scores of the lane's experts (0 for absent ones) and the factor that makes
 // them shares of 1.  A row whose logits are all -inf has no scores: all 0.
 template <int EPT>
@@ -300,7 +304,7 @@ __device__ __forceinline__ float scores(int score, int E, const float (&h)[EPT],
     } else {
 #pragma unroll
         for (int j = 0; j < EPT; ++j) {
-            s[j] = lane * EPT + j < E ? 1.f / (1.f + expf(-h[j])) : 0.f;
+            s[j] = lane * EPT + j < E ? sigmoid(h[j]) : 0.f;
             z += s[j];
         }
     }
@@ -337,13 +341,6 @@ __device__ __forceinline__ void get_row(const float *row, float (&v)[EPT]) {
     }
 }
 
-// 1 / (1 + exp(-l)): ex2 and rcp approximations, flushing below 2^-126.
-__device__ __forceinline__ float fast_sigmoid(float l) {
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-    return s;
-}
 // The 64-bit key of a logit.
 __device__ __forceinline__ double key64(const RouteArgs &a, float l, int e) {
     const double k = a.score == MOE_SCORE_SOFTMAX ? (double)l : 1.0 / (1.0 + exp(-(double)l));
@@ -356,16 +353,16 @@ __device__ __forceinline__ float one_logit(const RouteArgs &a, int t, int e) {
     return h;
 }
 
-// Error bounds.  A sigmoid key: ex2 of a rounded product is off by (2 + 1.2 |l|)
-// ulp, which moves s by s (1 - s) of that, at most 1.3 * 2^-24; the sum rounds by
-// 2^-24, rcp by an ulp: together below 4.3 * 2^-24 (s <= 1); the sum with the bias
-// by 2^-24 of it.  A softmax key: the latter alone.  Two distances from the best
-// key mx: besides their keys, cut off at 2^-15 of them and one rounding (and 2^-140,
-// what the cut takes off a subnormal one).
+// Error bounds.  A sigmoid key: expf is off by 4 * 2^-24 of its value (2 ulp), which
+// moves s by s (1 - s) of that, at most 2^-24; the sum and the quotient round by
+// 2^-24 each: together at most 3 * 2^-24 (s <= 1); the sum with the bias by 2^-24 of
+// it.  A softmax key: the latter alone.  Two distances from the best key mx: besides
+// their keys, cut off at 2^-15 of them and one rounding (and 2^-140, what the cut
+// takes off a subnormal one).
 struct Bounds {
     float abs, rel;                                // of a key
     __device__ __forceinline__ explicit Bounds(const RouteArgs &a)
-        : abs(a.score == MOE_SCORE_SOFTMAX ? 0.f : 0x1p-21f),
+        : abs(a.score == MOE_SCORE_SOFTMAX ? 0.f : 0x1p-22f),
           rel(a.score == MOE_SCORE_SOFTMAX && !a.sel_bias ? 0.f : 0x1p-23f) {}
     __device__ __forceinline__ float two(float mx) const { return 2.f * abs + 2.f * rel * fabsf(mx) + 0x1p-140f; }
     __device__ __forceinline__ float two_rel() const { return 0x1.2p-14f + 2.f * rel; }
@@ -507,14 +504,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1024 / (WARPS * 32)) route_select_
         } else {
             float z = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPT; ++j) { s[j] = fast_sigmoid(h[j]); z += s[j]; }      // absent experts: 0
-            z = warp_sum(z);
-            const float inv = z == 0.f ? 0.f : 1.f / z;
-#pragma unroll
-            for (int j = 0; j < EPT; ++j) {
-                share[j] = fmaf(s[j], inv, share[j]);
+            for (int j = 0; j < EPT; ++j) {        // absent experts: score 0
+                s[j] = sigmoid(h[j]);
+                z += s[j];
                 key[j] = FULL || lane * EPT + j < a.E ? s[j] + sb[j] : -INFINITY;
             }
+            z = warp_sum(z);
+            if (z < 0x1p-64f) {                    // gates and shares are ratios: keep 1 / z finite
+                z *= 0x1p64f;
+#pragma unroll
+                for (int j = 0; j < EPT; ++j) s[j] *= 0x1p64f;
+            }
+            const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) share[j] = fmaf(s[j], inv, share[j]);
         }
         put_row<EPT>(part[warp], s);
         float mx = key[0];
