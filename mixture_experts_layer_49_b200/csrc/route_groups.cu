@@ -623,20 +623,21 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
         const float dot = warp_sum(dg * g);
         dg = (used && sum != 0.f) ? (dg - dot) / sum : 0.f;
     }
-    // the chosen experts' gradients to their lanes
+    // the chosen experts' gradients to their lanes; an id that stands twice shows by
+    // the lane numbers of its slots (one of them overwrites the other's)
     __syncwarp();
     put_row<EPT>(row, ds);
-    if (used) row[e] = dg;
+    int *tag = reinterpret_cast<int *>(row);
+    if (used) tag[e] = lane;
     __syncwarp();
-    const unsigned same = __match_any_sync(kAll, used ? e : -1 - lane);
-    if (__any_sync(kAll, (same & (same - 1u)) != 0u)) {        // an id twice: slots in order
-        if (used) row[e] = 0.f;
-        __syncwarp();
-        for (int r = 0; r < a.k; ++r) {
+    const bool twice = __any_sync(kAll, used && tag[e] != lane);
+    if (used) row[e] = twice ? 0.f : dg;
+    __syncwarp();
+    if (twice)
+        for (int r = 0; r < a.k; ++r) {            // slots in order
             if (lane == r && used) row[e] += dg;
             __syncwarp();
         }
-    }
     get_row<EPT>(row, ds);
     if (a.alpha != 0.f) {
         const float c = a.balance;                 // alpha E / (T T k)
