@@ -289,6 +289,8 @@ __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)
 
 // Scores of the lane's experts (0 for absent ones) and the factor that makes
 // them shares of 1.  A row whose logits are all -inf has no scores: all 0.
+// Sigmoids that are tiny everywhere come times 2^64 (their ratios count), so
+// that the factor stays finite.
 template <int EPT>
 __device__ __forceinline__ float scores(int score, int E, const float (&h)[EPT], float (&s)[EPT]) {
     const int lane = threadIdx.x & 31;
@@ -309,6 +311,11 @@ __device__ __forceinline__ float scores(int score, int E, const float (&h)[EPT],
         }
     }
     z = warp_sum(z);
+    if (z < 0x1p-64f && score != MOE_SCORE_SOFTMAX) {
+        z *= 0x1p64f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) s[j] *= 0x1p64f;
+    }
     return z == 0.f ? 0.f : 1.f / z;
 }
 
@@ -586,8 +593,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1024 / (WARPS * 32)) route_select_
 }
 
 // dlogits of ell = sum dgate * gate + alpha * E * sum_e f_e P_e; the choice of
-// experts and f_e = counts_e / (T k) carry no gradient.  With ds the gradient
-// of the scores: softmax dl = s (ds - <ds, s>), sigmoid dl = ds s (1 - s).
+// experts and f_e = counts_e / (T k) carry no gradient.  With v_e the sum over
+// the slots of e of
+//   c dg s               softmax, renorm 0
+//   (c dg - <c dg, g>) g else, g the gates before their factor c
+// and cf_e = alpha E f_e / T:
+//   softmax  dl = v + s (cf - <cf, s> - sum v)    (sum v is 0 with renorm)
+//   sigmoid  dl = (v + q (cf - <cf, q>)) (1 - s), q = s / sum s
+// Scores enter as shares alone, so no quotient passes the fp32 range where all
+// of a row's, or all chosen, sigmoids are tiny.
 template <int EPT>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
     pdl_wait_then_release();
@@ -616,56 +630,43 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwdArgs a) {
         ds[j] = 0.f;
     }
     put_row<EPT>(row, s);
-    if (!softmax || a.renorm) {
-        const float sv = row[e];
+    const float sv = row[e];
+    const bool renorm = !softmax || a.renorm;
+    float g = sv;
+    if (renorm) {
         const float sum = warp_sum(used ? sv : 0.f);
-        const float g = sum == 0.f ? 0.f : sv / sum;
-        const float dot = warp_sum(dg * g);
-        dg = (used && sum != 0.f) ? (dg - dot) / sum : 0.f;
+        g = sum == 0.f ? 0.f : sv / sum;
+        dg -= warp_sum(dg * g);
     }
+    const float v = used ? dg * g : 0.f;
     // the chosen experts' gradients to their lanes; an id that stands twice shows by
     // the lane numbers of its slots (one of them overwrites the other's)
     __syncwarp();
     put_row<EPT>(row, ds);
-    int *tag = reinterpret_cast<int *>(row);
-    if (used) tag[e] = lane;
+    if (used) row[e] = __int_as_float(lane);
     __syncwarp();
-    const bool twice = __any_sync(kAll, used && tag[e] != lane);
-    if (used) row[e] = twice ? 0.f : dg;
+    const bool twice = __any_sync(kAll, used && __float_as_int(row[e]) != lane);
+    if (used) row[e] = twice ? 0.f : v;
     __syncwarp();
     if (twice)
         for (int r = 0; r < a.k; ++r) {            // slots in order
-            if (lane == r && used) row[e] += dg;
+            if (lane == r && used) row[e] += v;
             __syncwarp();
         }
     get_row<EPT>(row, ds);
-    if (a.alpha != 0.f) {
-        const float c = a.balance;                 // alpha E / (T T k)
-        float cf[EPT], dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            cf[j] = lane * EPT + j < a.E ? c * (float)__ldg(a.counts + lane * EPT + j) : 0.f;
-            dot += cf[j] * s[j];
-        }
-        if (softmax) {
-#pragma unroll
-            for (int j = 0; j < EPT; ++j) ds[j] += cf[j];
-        } else {
-            dot = warp_sum(dot) * inv;
-#pragma unroll
-            for (int j = 0; j < EPT; ++j) ds[j] += (cf[j] - dot) * inv;
-        }
-    }
-    float dot = 0.f;
-    if (softmax) {
-#pragma unroll
-        for (int j = 0; j < EPT; ++j) dot += ds[j] * s[j];
-        dot = warp_sum(dot);
-    }
+    float cf[EPT], dot = renorm ? 0.f : v;
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
-        if (softmax) ds[j] = s[j] * (ds[j] - dot);
-        else ds[j] *= s[j] * (1.f / (1.f + expf(h[j])));     // 1 - s without its cancellation near s = 1
+        cf[j] = 0.f;
+        if (a.alpha != 0.f && lane * EPT + j < a.E) cf[j] = a.balance * (float)__ldg(a.counts + lane * EPT + j);
+        dot = fmaf(cf[j], s[j], dot);
+    }
+    if (!renorm || a.alpha != 0.f) dot = warp_sum(dot);
+    if (!softmax) dot *= inv;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        if (softmax) ds[j] += s[j] * (cf[j] - dot);
+        else ds[j] = (ds[j] + s[j] * inv * (cf[j] - dot)) * (1.f / (1.f + expf(h[j])));     // 1 - s without its cancellation near s = 1
     }
     float *o = a.dlogits + (size_t)t * a.E + lane * EPT;
     if (EPT >= 4 && a.vec_out) {

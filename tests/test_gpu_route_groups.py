@@ -291,3 +291,44 @@ def test_sigmoid_scores_of_any_size(cuda_device, lo, hi):
         assert ((gate.cpu().double() - want).abs() <= want * 2.0 ** -19).all()
         want = ref.score_sums(logits.cpu(), "sigmoid")
         assert ((psum.cpu().double() - want).abs() <= want * 2.0 ** -17 + 1e-37).all()
+
+
+@pytest.mark.parametrize("alpha", [0.0, 0.5])
+def test_gradient_of_tiny_sigmoids(cuda_device, alpha):
+    """Rows whose sigmoids are all tiny, and rows whose chosen ones are tiny beside
+    the others': the same bound as test_gradient (scores below 2^-126 lose
+    2^-22 of their value, within it).  Below -88.72 the fp32 score is 0: such rows'
+    gradients are finite, and 0 where nothing chosen is left and alpha is 0."""
+    T, E, k, scale = 64, 256, 8, 16.0
+    g = torch.Generator(device=cuda_device).manual_seed(41)
+    cfg, groups = config(T, E, k, "sigmoid", 1), nat.route_groups(1, 1, 1, scale)
+    dgate = torch.randn((T, k), generator=g, device=cuda_device)
+    d = torch.empty((T, E), device=cuda_device)
+
+    def backward(logits, idx):
+        counts = torch.bincount(idx.flatten().long(), minlength=E).to(torch.int32)
+        nat.moe_route_backward(cfg, groups, logits, idx, dgate, counts if alpha else None, alpha, d)
+        return counts.cpu()
+
+    low = -88.7 + 0.4 * torch.rand((T, E), generator=g, device=cuda_device)
+    wide = -88.7 + 30.0 * torch.rand((T, E), generator=g, device=cuda_device)
+    mixed = 3.0 * torch.randn((T, E), generator=g, device=cuda_device)
+    mixed[:, 128:] = low[:, 128:]
+    for logits in (low, wide, mixed):
+        idx = 128 + torch.rand((T, 128), generator=g, device=cuda_device).topk(k, 1).indices.to(torch.int32)
+        counts = backward(logits, idx)
+        want = ref.route_backward(logits.cpu(), idx.cpu(), dgate.cpu(), counts, alpha, "sigmoid", 1, scale)
+        s = ref.scores(logits.cpu(), "sigmoid")
+        total = s.gather(1, idx.cpu().long()).sum(1, keepdim=True)
+        own = torch.zeros_like(s).scatter_add_(1, idx.cpu().long(), dgate.cpu().double().abs() * scale / total)
+        mean = (own * s).sum(1, keepdim=True)
+        bal = alpha * E / T * counts.double() / (T * k)
+        z = s.sum(1, keepdim=True)
+        hit = torch.zeros_like(s).scatter_(1, idx.cpu().long(), 1.0)
+        size = s * (1 - s) * (own + hit * mean / total + (bal + (bal * s).sum(1, keepdim=True) / z) / z)
+        assert ((d.cpu().double() - want).abs() <= size * 2.0 ** -15 + 1e-37).all()
+    idx = torch.arange(k, dtype=torch.int32, device=cuda_device).repeat(T, 1).contiguous()
+    for lo, hi in ((-100.0, -80.0), (-200.0, -89.0)):
+        backward(lo + (hi - lo) * torch.rand((T, E), generator=g, device=cuda_device), idx)
+        assert torch.isfinite(d).all()
+    assert alpha or (d == 0).all()
