@@ -332,3 +332,33 @@ def test_gradient_of_tiny_sigmoids(cuda_device, alpha):
         backward(lo + (hi - lo) * torch.rand((T, E), generator=g, device=cuda_device), idx)
         assert torch.isfinite(d).all()
     assert alpha or (d == 0).all()
+
+
+@pytest.mark.parametrize("E,size", [(32, 4), (256, 32), (60, 12)])
+def test_masks_of_the_lowest_value_beside_infinite_ones(cuda_device, E, size):
+    """Sums of two of the lowest fp32 values, and differences from large keys, pass the
+    fp32 range; the 64-bit keys still rank them above -inf and among themselves."""
+    lowest, inf = torch.finfo(torch.float32).min, float("inf")
+    n = E // size
+    grp = lambda g: slice(g * size, (g + 1) * size)
+    l = torch.full((8, E), -inf)
+    l[0, grp(2)] = lowest                                       # one group at the lowest value, one real
+    l[1, grp(1)], l[1, grp(3)] = lowest, lowest / 2             # two masked groups, by id and by key
+    l[2, grp(1)], l[2, grp(3)] = lowest / 2, lowest
+    l[3, 0], l[3, E - 2] = lowest, 2e38
+    l[4] = lowest
+    l[4, grp(3)] = lowest / 2
+    l[5] = lowest
+    l[5, 4], l[5, 2 * size] = 1.0, lowest / 2
+    l[6] = lowest
+    l[6, ::3] = -inf
+    l[7] = torch.linspace(-3.4e38, -3.0e38, E)
+    for t, v in ((0, 1.0), (1, 1.0), (2, 1.0), (3, 3e38), (4, 1.0)):
+        l[t, E - 1] = v
+        l[t, E - 2] = v / 2
+    l = l.to(cuda_device)
+    for topk_group, group_top in ((1, 2), (2, 2), (3, 2), (2, 1), (n, 1)):
+        for k in (1, 2, 4, min(8, size)):
+            idx, _, _ = run(l, None, k, (n, topk_group, group_top, 1.0), "softmax")
+            want = ref.select(l.cpu(), None, k, n, topk_group, group_top, "softmax")
+            assert torch.equal(idx.cpu(), want), (topk_group, group_top, k)
