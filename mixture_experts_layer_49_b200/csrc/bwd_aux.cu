@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
     for (int i = 0; i < EPL; ++i) mx = fmaxf(mx, h[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (mx == -INFINITY) mx = 0.f;                 // a row without scores: all 0, as in the forward pass
     float norm = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
         norm += sc[i];
     }
     norm = warp_sum(norm);
-    if (a.score == MOE_SCORE_SOFTMAX) {
+    if (a.score == MOE_SCORE_SOFTMAX && norm != 0.f) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) sc[i] /= norm;
     }
@@ -158,17 +159,20 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
         const float dot = warp_sum(in_slot ? gs * dgs : 0.f);
         float ssel = 0.f;
         for (int s = 0; s < k; ++s) ssel += score_of(sc, __shfl_sync(0xffffffffu, es, s));
+        const float up = ssel < 0x1p-64f ? 0x1p64f : 1.f;      // a tiny sum: the quotient stays finite
+        ssel *= up;
         for (int s = 0; s < k; ++s) {
             const int e = __shfl_sync(0xffffffffu, es, s);
             // no scores left (every chosen sigmoid underflowed): gates of 0, no gradient
             const float v = __shfl_sync(0xffffffffu, ssel == 0.f ? 0.f : (dgs * a.gate_scale - dot) / ssel, s);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (i * 32 + lane == e) dh[i] += v * sc[i] * (1.f - sc[i]);
+                if (i * 32 + lane == e) dh[i] += v * (sc[i] * up) * (1.f - sc[i]);
         }
     }
     // balance loss through P: c_e = alpha E f_e / T, pnorm = p (softmax) or s / S_all
-    if (a.alpha != 0.f) {
+    if (a.alpha != 0.f && norm != 0.f) {
+        const float up = norm < 0x1p-64f ? 0x1p64f : 1.f, normu = norm * up;
         const float inv_T = 1.f / (float)a.T;
         float cv[EPL], cq = 0.f;
 #pragma unroll
@@ -176,14 +180,14 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(BwdAuxArgs a) {
             const int e = i * 32 + lane;
             const float f = e < E ? (float)a.counts[e] / ((float)a.T * (float)k) : 0.f;
             cv[i] = a.alpha * (float)E * f * inv_T;
-            const float q = a.score == MOE_SCORE_SOFTMAX ? sc[i] : sc[i] / norm;
+            const float q = a.score == MOE_SCORE_SOFTMAX ? sc[i] : sc[i] * up / normu;
             cq += cv[i] * q;
         }
         cq = warp_sum(cq);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             if (a.score == MOE_SCORE_SOFTMAX) dh[i] += sc[i] * (cv[i] - cq);
-            else dh[i] += (cv[i] - cq) / norm * sc[i] * (1.f - sc[i]);
+            else dh[i] += (cv[i] - cq) / normu * (sc[i] * up) * (1.f - sc[i]);
         }
     }
 #pragma unroll
