@@ -45,7 +45,7 @@ struct Layout {
     // e4m3 experts with a scale per block of 128 (codes in x8, x_perm and H8
     // as above): scale rows of x, of the packed rows and of H
     size_t xs, xs_perm, hs;
-    size_t h32;          // fp32 hidden rows of a few tokens
+    size_t h32;          // fp32 hidden rows of at most kFp8BlockDecodeT tokens
     size_t total;
 };
 
@@ -89,7 +89,9 @@ Layout layout(const moe_config *c) {
     L.xs = o;         o = align256(o + f8 * (size_t)c->T * scale_row_bytes(c->d_model));
     L.xs_perm = o;    o = align256(o + f8 * Tk * scale_row_bytes(c->d_model));
     L.hs = o;         o = align256(o + f8 * rows * scale_row_bytes((int)hF));
-    L.h32 = o;        o = align256(o + (c->T <= moe::kFp8BlockDecodeT ? f8 * rows * hF * 4 : 0));
+    // only calls of few tokens use it, but a workspace for more tokens serves them too
+    const size_t few = (size_t)std::min(c->T, moe::kFp8BlockDecodeT) * (c->top_k + (c->d_ff_shared > 0 ? 1 : 0));
+    L.h32 = o;        o = align256(o + f8 * few * hF * 4);
     L.total = o;
     return L;
 }

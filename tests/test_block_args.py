@@ -213,6 +213,15 @@ def test_scale_row_stride():
     assert w["Wsd"].shape == (272, 16) and w["Wsd_scale"].shape == (3, 4)
 
 
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("d,F,E,k,S", [(4096, 14336, 8, 2, 0), (2048, 8192, 8, 2, 0), (2048, 768, 128, 8, 0),
+                                       (7168, 2048, 32, 8, 2048), (128, 2048, 4, 1, 4096), (128, 256, 8, 2, 0)])
+def test_a_workspace_of_more_tokens_serves_fewer(d, F, E, k, S, act):
+    """One workspace for the largest batch: the size never falls as tokens are added."""
+    sizes = [nat.workspace_size(nat.make_config(T, d, E, F, k, act=act, d_ff_shared=S)) for T in range(300)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 # ---------------------------------------------------------------- reference gradients against differences
 def test_norm_gradient_is_the_difference_quotient():
     g = torch.Generator().manual_seed(3)

@@ -359,3 +359,17 @@ def test_repeated_calls_give_the_same_bits(cuda_device, T, d, E, F, k, act, S):
                                       r["xt8"], r["xts"], r["y"], r["ws"])
         assert torch.equal(r["y"], first)
     assert nat.moe_get_device_status(r["ws"]) == nat.MOE_OK
+
+
+def test_one_workspace_for_every_batch(cuda_device):
+    """A batch that shrinks keeps its workspace: the same bits as in one of its own."""
+    big = None
+    for T in (40, 3, 2, 1):
+        wl, cfg, inp, sld, w = layer(cuda_device, T=T)
+        if big is None:
+            big = nat.alloc_workspace(cfg)
+        out, own, ws = nat.Outputs(cfg), nat.Outputs(cfg), nat.alloc_workspace(cfg)
+        nat.forward_fp8_block(cfg, inp, w, sld, out, big)
+        nat.forward_fp8_block(cfg, inp, w, sld, own, ws)
+        assert nat.moe_get_device_status(big) == nat.MOE_OK
+        assert torch.equal(out.y, own.y) and torch.equal(out.idx, own.idx)
