@@ -373,3 +373,27 @@ def test_one_workspace_for_every_batch(cuda_device):
         nat.forward_fp8_block(cfg, inp, w, sld, own, ws)
         assert nat.moe_get_device_status(big) == nat.MOE_OK
         assert torch.equal(out.y, own.y) and torch.equal(out.idx, own.idx)
+
+
+@pytest.mark.parametrize("T,E,S", [(1, 64, 0), (2, 64, 0), (1, 200, 128), (2, 33, 128), (3, 64, 0)])
+def test_bad_offsets_of_few_tokens_are_recorded(cuda_device, T, E, S):
+    """Wherever the bad entry stands: before, at and after the experts with rows."""
+    wl = syn.Workload("block", T=T, d_model=256, E=E, d_ff=256, top_k=1, d_ff_shared=S)
+    cfg = nat.config_from_workload(wl)
+    sld = nat.fp8_block_sld(cfg)
+    w = syn.generate_fp8_block_experts(wl, sld, cuda_device)
+    r = grouped(cfg, None, [T] + [0] * (E - 1), w, sld, cuda_device, 1, False)
+    good, offsets = r["y"].clone(), r["offsets"].clone()
+
+    def call():
+        nat.moe_grouped_ffn_fp8_block(cfg, r["x8"], r["xs"], r["offsets"], r["gate"], r["ex"], None, None, r["xt8"],
+                                      r["xts"], r["y"], r["ws"])
+        return nat.moe_get_device_status(r["ws"])
+
+    for at in (0, 1, 2, 31, 32, E // 2, E - 1, E):
+        for bad in (-1, T + 4) + ((T - 1,) if at > 1 else ()):
+            r["offsets"].copy_(offsets)
+            r["offsets"][at] = bad
+            assert call() == nat.MOE_ERR_DEVICE_BOUNDS, (at, bad)
+    r["offsets"].copy_(offsets)
+    assert call() == nat.MOE_OK and torch.equal(r["y"], good)
