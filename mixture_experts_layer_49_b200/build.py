@@ -15,7 +15,7 @@ SOURCES = ["moe_api.cu", "router_topk.cu", "dispatch.cu", "ffn_f32.cu", "ffn_sm1
            "combine_balance.cu", "permute_noalloc.cu", "router_sm100.cu", "quant_fp8.cu",
            "bwd_sm100.cu", "bwd_aux.cu", "bwd_api.cu", "mx_sm100.cu", "rmsnorm.cu", "route_groups.cu",
            "fp8_block.cu", "fp8_block_sm100.cu", "fp8_block_decode.cu", "block_api.cu"]
-HEADERS = ["balance.cuh", "common.cuh", "kernels.cuh", "sm100.cuh"]
+HEADERS = ["balance.cuh", "common.cuh", "fp8_block.cuh", "kernels.cuh", "sm100.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

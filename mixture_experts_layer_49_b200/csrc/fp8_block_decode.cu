@@ -24,6 +24,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp8_block.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -55,9 +56,6 @@ struct Params {
     __nv_bfloat16 *out;                        // y rows (second product)
     int64_t ldo;
 };
-
-__device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * (1.f + erff(v * 0.70710678118654752f)); }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
 __device__ __forceinline__ void mma_e4m3_16x8x32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                  uint32_t b0, uint32_t b1) {
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_block_decode(const __grid_con
                 const float gate = sh ? 1.f : __ldg(p.row_gate + row);
                 p.out[orow * p.ldo + col] = __float2bfloat16_rn((v[0] + bias) * gate);
             } else {
-                p.out_h[orow * p.ldh + col] = MODE == FB_SWIGLU ? silu(v[0]) * v[NM - 1] : gelu_erf(v[0] + bias);
+                p.out_h[orow * p.ldh + col] = MODE == FB_SWIGLU ? fb_silu(v[0]) * v[NM - 1] : fb_gelu(v[0] + bias);
             }
         }
         __syncthreads();

@@ -44,6 +44,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "fp8_block.cuh"
 #include "kernels.cuh"
 #include "sm100.cuh"
 
@@ -112,19 +113,6 @@ constexpr uint32_t STG_BYTES = 32 * 64;
 constexpr size_t kStgOff = (STAGES * STAGE_BYTES + sizeof(Tail) + 1023) / 1024 * 1024;
 constexpr size_t kSmemBytes = 1024 + kStgOff + 8 * STG_BYTES;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-
-// v Phi(v) with Abramowitz and Stegun's rational form 7.1.26 of erfc (off by at
-// most 1.5e-7, so the result by 2^-23.6 |v|, far below an e4m3 step); erff took
-// two thirds of a GELU tile's epilogue.
-__device__ __forceinline__ float gelu_erf(float v) {
-    const float z = fabsf(v) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                0.254829592f);
-    const float q = 0.5f * poly * __expf(-z * z);          // the smaller tail, Phi(-|v|)
-    return v * (v < 0.f ? q : 1.f - q);
-}
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
 // One lane of the converged warp, always the same one.
 __device__ __forceinline__ bool elect_lane() {
@@ -270,7 +258,7 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
     if (MODE == FB_SWIGLU) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-            acc[i] = silu(acc[i]) * acc[64 + i];
+            acc[i] = fb_silu(acc[i]) * acc[64 + i];
             amax = fmaxf(amax, fabsf(acc[i]));             // columns past N are 0 * 0
         }
         // the block's maximum spans the two halves of the row; an mbarrier,
@@ -292,7 +280,7 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
         }
 #pragma unroll
         for (int i = 0; i < 128; ++i) {
-            acc[i] = gelu_erf(acc[i]);                     // columns past N: gelu(0) = 0
+            acc[i] = fb_gelu(acc[i]);                      // columns past N: gelu(0) = 0
             amax = fmaxf(amax, fabsf(acc[i]));
         }
     }

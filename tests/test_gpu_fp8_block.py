@@ -5,6 +5,8 @@ and a bound on what fp32 sums and the codes of H that lie within such a sum's
 error of a rounding border can change (block_reference.ffn); the gate's product
 adds 2^-24 and the bf16 rounding 2^-8 of the value.
 """
+import math
+
 import pytest
 import torch
 
@@ -397,3 +399,42 @@ def test_bad_offsets_of_few_tokens_are_recorded(cuda_device, T, E, S):
             assert call() == nat.MOE_ERR_DEVICE_BOUNDS, (at, bad)
     r["offsets"].copy_(offsets)
     assert call() == nat.MOE_OK and torch.equal(r["y"], good)
+
+
+def test_gelu_in_its_tails(cuda_device):
+    """Zero weights and b1 alone: every block of 128 hidden values is one GELU value,
+    which the second product (the identity) returns as 448 * scale.  b2 takes the
+    exact value away, so y is the error, in the units of the value: GELU 17 * 2^-24
+    (at most 32 by its terms), scale, product, sum and b2 one each: below 2^-18.
+    One, two and more tokens give the same bits."""
+    d = 2048
+    first = None
+    for T, sign in ((1, -1), (2, -1), (3, -1), (300, -1), (3, 1), (1, 1)):
+        wl = syn.Workload("block", T=T, d_model=d, E=8, d_ff=d, top_k=1, act="gelu")
+        cfg = nat.config_from_workload(wl)
+        sld = nat.fp8_block_sld(cfg)
+        w = syn.generate_fp8_block_experts(wl, sld, cuda_device)
+        w["W1"].zero_(), w["W2"].zero_()
+        i = torch.arange(d, device=cuda_device)
+        w["W2"][:, i, i] = 0x38                                             # 1.0
+        w["W2_scale"].fill_(1.0)
+        v = sign * torch.linspace(0.01, 9.0, 8 * d // 128).view(8, -1)
+        a = v.repeat_interleave(128, 1)
+        h = 0.5 * a.double() * torch.erfc(-a.double() / math.sqrt(2.0))
+        w["b1"], w["b2"] = a.to(cuda_device).contiguous(), (-h).float().to(cuda_device).contiguous()
+        counts = [0] * 8
+        got = []
+        for e in range(8):
+            counts[e] = T
+            r = grouped(cfg, None, counts, w, sld, cuda_device, 1, True)
+            r["gate"].fill_(1.0)
+            nat.moe_grouped_ffn_fp8_block(cfg, r["x8"], r["xs"], r["offsets"], r["gate"], r["ex"], w["b1"], w["b2"], None,
+                                          None, r["y"], r["ws"])
+            assert (r["y"] == r["y"][:1]).all()
+            got.append(r["y"][0].cpu().double())
+            counts[e] = 0
+        got = torch.stack(got)
+        assert (got.abs() <= h.abs() * 2.0 ** -18).all(), (got / h).abs().max()
+        if sign < 0:
+            first = got if first is None else first
+            assert torch.equal(got, first)
