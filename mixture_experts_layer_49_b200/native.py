@@ -771,7 +771,7 @@ def fp8_block_experts(w, sld) -> MoeFp8BlockExperts:
     call takes the experts; it keeps the tensors alive."""
     dev = _current_device()
     s = MoeFp8BlockExperts()
-    s._tensors = []
+    s._tensors, s._sizes, s._fits = [], {}, None
     for name in FP8_WEIGHTS:
         field = _FP8_FIELD[name]
         codes, scale = w.get(name), w.get(name + "_scale")
@@ -780,8 +780,26 @@ def fp8_block_experts(w, sld) -> MoeFp8BlockExperts:
         setattr(s, field, _arg(codes, name, dev, _CODES))
         setattr(s, field + "_scale", _arg(scale, name + "_scale", dev, _F32, blocks * int(sld) // 4))
         s._tensors += [codes, scale]
+        s._sizes[name] = tuple(0 if t is None else t.numel() for t in (codes, scale))
     s.sld = int(sld)
     return s
+
+
+def _fit_block_experts(cfg, w):
+    """Raises where fp8_block_experts' tensors are smaller than the layer's."""
+    sizes = getattr(w, "_sizes", None)             # None: a struct of the caller's own pointers
+    d, E, F, S = cfg.d_model, cfg.E, cfg.d_ff, cfg.d_ff_shared
+    if sizes is None or w._fits == (d, E, F, S, w.sld):
+        return
+    for name, n, rows, cols in (("W1", E, F, d), ("Wu", E, F, d), ("W2", E, d, F), ("Wsg", 1, S, d), ("Wsu", 1, S, d),
+                                ("Wsd", 1, d, S)):
+        codes, scale = sizes[name]
+        need = n * ((rows + 127) // 128) * w.sld // 4 if cols else 0
+        if codes and codes < n * rows * cols:
+            raise ValueError("%s holds %d elements, %d are needed" % (name, codes, n * rows * cols))
+        if scale and scale < need:
+            raise ValueError("%s_scale holds %d elements, %d are needed" % (name, scale, need))
+    w._fits = (d, E, F, S, w.sld)
 
 
 def _block_experts(w, sld=None) -> MoeFp8BlockExperts:
@@ -810,6 +828,7 @@ def moe_quantize_rows_block(x, codes, scale, rows=None, cols=None, ld_in=None, l
 def moe_grouped_ffn_fp8_block(cfg, x8_perm, xs_perm, offsets, row_gate, w, b1, b2, x8, xs, y_perm, ws, stream=None):
     """moe_grouped_ffn_fp8_block; w: fp8_block_experts(...)."""
     dev = _current_device()
+    _fit_block_experts(cfg, w)
     T, d, E = cfg.T, cfg.d_model, cfg.E
     rows, spr = T * cfg.top_k, w.sld // 4
     _check(lib().moe_grouped_ffn_fp8_block(
@@ -825,6 +844,7 @@ def moe_forward_fp8_block(cfg, groups, x, x8, xs, Wr, logit_bias, sel_bias, w, b
                           loss, logits_out, n_dropped, ws, stream=None):
     """moe_forward_fp8_block; groups may be None, x8 and xs may both be None."""
     dev = _current_device()
+    _fit_block_experts(cfg, w)
     T, d, E, k = cfg.T, cfg.d_model, cfg.E, cfg.top_k
     _check(lib().moe_forward_fp8_block(
         ctypes.byref(cfg), None if groups is None else ctypes.byref(groups), _arg(x, "x", dev, _BF16, T * d),

@@ -203,6 +203,38 @@ def test_binding_refuses_host_tensors_and_sizes():
         nat.fp8_block_experts(dict(W1=torch.zeros(8, 16, 16, dtype=torch.uint8)), 16)
 
 
+def test_binding_refuses_experts_smaller_than_the_layer(monkeypatch):
+    """Host tensors stand in for device tensors: no call gets as far as a launch."""
+    monkeypatch.setattr(nat, "_current_device", lambda: -1)
+    wl = syn.Workload("block", T=4, d_model=272, E=4, d_ff=144, top_k=1, d_ff_shared=16)
+    c, sld = nat.config_from_workload(wl), 16
+    full = syn.generate_fp8_block_experts(wl, sld)
+
+    def ffn(w):
+        nat.moe_grouped_ffn_fp8_block(c, None, None, None, None, nat.fp8_block_experts(w, sld), None, None, None, None, None,
+                                      torch.zeros(256, dtype=torch.uint8))
+
+    def forward(w):
+        nat.moe_forward_fp8_block(c, None, *[None] * 6, nat.fp8_block_experts(w, sld), *[None] * 11,
+                                  torch.zeros(256, dtype=torch.uint8))
+
+    for name in ("W1", "Wu", "W2"):
+        less = {name: full[name][:3].contiguous(), name + "_scale": full[name + "_scale"][:3].contiguous()}
+        for call in (ffn, forward):
+            with pytest.raises(ValueError, match=name):
+                call(dict(full, **less))
+    for name in ("Wsg", "Wsu", "Wsd"):
+        less = {name: full[name][:, :8].contiguous()}
+        for call in (ffn, forward):
+            with pytest.raises(ValueError, match=name):
+                call(dict(full, **less))
+    short = dict(full, W2=full["W2"].reshape(4, 144, 272))                  # one block of rows fewer than its shape
+    short["W2_scale"] = full["W2_scale"][:, :2].contiguous()
+    for call in (ffn, forward):
+        with pytest.raises(ValueError, match="W2_scale"):
+            call(short)
+
+
 def test_scale_row_stride():
     assert nat.fp8_block_sld(cfg()) == 16
     assert nat.fp8_block_sld(cfg(d_model=7168)) == 224
