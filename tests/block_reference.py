@@ -164,11 +164,15 @@ def _product(x, w, blocks):
     return x @ w.T, (x.abs() @ w.abs().T) * (blocks + 16) * 2.0 ** -23
 
 
-def ffn(x, w1, wu, w2, b1, b2):
+def ffn(x, w1, wu, w2, b1, b2, far=False):
     """Output rows of one expert on dequantized rows x, and a bound on how far
     a computation with fp32 sums may be off before its last rounding.  A hidden
     value within its fp32 error of the middle between two codes may take either
-    code: the bound adds that step times its weights."""
+    code: the bound adds that step times its weights.
+
+    far: for arguments of the SiLU beyond 90 as well.  exp(-a) is 0 or infinite
+    there, so the result is a, or 0 where the exact value is below 90 e^-90 |u|,
+    and its error grows no further with |a|; and codes saturate at -448 as at 448."""
     blocks = (x.shape[1] + 127) // 128
     a, ea = _product(x, w1, blocks)
     if wu is None:
@@ -180,14 +184,14 @@ def ffn(x, w1, wu, w2, b1, b2):
         u, eu = _product(x, wu, blocks)
         s = a / (1.0 + torch.exp(-a))
         h = s * u
-        eh = 1.1 * ea * u.abs() + s.abs() * eu + h.abs() * (10 + 1.5 * a.abs()) * 2.0 ** -23
+        eh = 1.1 * ea * u.abs() + s.abs() * eu + h.abs() * (10 + 1.5 * (a.abs().clamp(max=90.0) if far else a.abs())) * 2.0 ** -23
     width = h.shape[1]
     top = block_max(h)
     etop = block_max(eh)                            # the maximum moves by at most the largest error
     rel = spread(etop / top, width)
     q = h * spread(448.0 / top, width)
     eq = eh * spread(448.0 / top, width) + q.abs() * (rel + 2.0 ** -22)
-    lo = (q - eq).to(torch.float32).to(torch.float8_e4m3fn).to(F64)
+    lo = (q - eq).clamp(min=-448.0 if far else -math.inf).to(torch.float32).to(torch.float8_e4m3fn).to(F64)
     hi = (q + eq).clamp(max=448.0).to(torch.float32).to(torch.float8_e4m3fn).to(F64)
     mid = q.to(torch.float32).to(torch.float8_e4m3fn).to(F64)
     flip = torch.maximum(hi - mid, mid - lo)

@@ -71,7 +71,7 @@ def grouped(cfg, rows, counts, w, sld, dev, seed, gelu, shared=None):
     return dict(x8=x8, xs=xs, gate=gate, y=y, xt8=xt8, xts=xts, offsets=offsets, ws=ws, ex=ex)
 
 
-def check(cfg, counts, w, r):
+def check(cfg, counts, w, r, far=False):
     h = {k: v.cpu() for k, v in w.items()}
     y = r["y"].cpu().double()
     x = ref.dequantize(r["x8"].cpu(), r["xs"].cpu())
@@ -83,7 +83,7 @@ def check(cfg, counts, w, r):
             continue
         m = [ref.dequantize_weight(h[k][e], h[k + "_scale"][e]) if k in h else None for k in names]
         b = (h["b1"][e], h["b2"][e]) if "b1" in h else (None, None)
-        want, err = ref.ffn(x[at:at + n], *m, *b)
+        want, err = ref.ffn(x[at:at + n], *m, *b, far)
         want, err = want * gate[at:at + n], err * gate[at:at + n]
         off = (y[at:at + n] - want).abs()
         assert (off <= want.abs() * HALF * (1 + 2.0 ** -15) + err * (1 + HALF) + 1e-30).all(), (e, (off - err).max())
@@ -438,3 +438,18 @@ def test_gelu_in_its_tails(cuda_device):
         if sign < 0:
             first = got if first is None else first
             assert torch.equal(got, first)
+
+
+def test_scales_forty_binary_orders_apart(cuda_device):
+    """Weight scales spread over 2^-20 .. 2^20."""
+    wl = syn.Workload("block", T=140, d_model=400, E=2, d_ff=272, top_k=1)
+    cfg = nat.config_from_workload(wl)
+    sld = nat.fp8_block_sld(cfg)
+    w = syn.generate_fp8_block_experts(wl, sld, cuda_device, seed=4)
+    g = torch.Generator(device=cuda_device).manual_seed(10)
+    for name in ("W1_scale", "Wu_scale", "W2_scale"):
+        w[name] *= torch.exp2(torch.randint(-20, 21, w[name].shape, generator=g, device=cuda_device).float())
+    check(cfg, [139, 1], w, grouped(cfg, None, [139, 1], w, sld, cuda_device, 5, False), far=True)
+    wl = syn.Workload("block", T=2, d_model=400, E=2, d_ff=272, top_k=1)     # and the form for few tokens
+    cfg = nat.config_from_workload(wl)
+    check(cfg, [1, 1], w, grouped(cfg, None, [1, 1], w, sld, cuda_device, 6, False), far=True)

@@ -204,3 +204,21 @@ def test_graph_streams_and_refusals(cuda_device):
         args.update(bad)
         with pytest.raises((ValueError, nat.MoEError)):
             nat.moe_rmsnorm(**args)
+
+
+# dw of many rows.  A part of the launch takes every parts-th row, one multiply-add
+# each; there is at least one part per SM (or per row), so ceil(T / SMs) roundings.
+# Then 32 groups of the at most 1184 parts (more below 512 columns: 9472) in turn, and
+# the groups: at most ceil(parts / 32) + 32.  n carries 2^-18.
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(6000, 64), (5000, 1032), (5000, 4104), (4100, 7168), (3000, 8200), (700, 32768)])
+def test_weight_gradient_of_many_rows(cuda_device, T, d, dt):
+    h, dy = (rows_of(T, d, dt, cuda_device, s) for s in (17, 18))
+    w = 1.0 + 0.1 * torch.randn(d, device=cuda_device)
+    dh, dw = backward(h, w, dy, None)
+    want, wantw, size, sizew = ref.rmsnorm_backward(h.cpu(), w.cpu(), EPS, dy.cpu(), None)
+    assert ((dh.cpu().double() - want).abs() <= want.abs() * HALF[dt] * (1 + 2.0 ** -16) + size * 2.0 ** -17).all()
+    sms = torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    parts = 1184 if d >= 512 else 9472
+    adds = -(-T // sms) + -(-parts // 32) + 32
+    assert ((dw.cpu().double() - wantw).abs() <= sizew * (adds * 2.0 ** -24 + FP32)).all()
