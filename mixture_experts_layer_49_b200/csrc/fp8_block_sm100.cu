@@ -279,9 +279,9 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
             for (int i = 0; i < 128; ++i) acc[i] += col0 + i < c.N ? __ldg(c.bias + col0 + i) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
-            acc[i] = fb_gelu(acc[i]);                      // columns past N: gelu(0) = 0
-            amax = fmaxf(amax, fabsf(acc[i]));
+        for (int i = 0; i < 128; i += 2) {
+            fb_gelu2(acc[i], acc[i + 1]);                  // columns past N: gelu(0) = 0
+            amax = fmaxf(amax, fmaxf(fabsf(acc[i]), fabsf(acc[i + 1])));
         }
     }
     amax = fmaxf(amax, 0x1p-100f);

@@ -404,8 +404,8 @@ def test_bad_offsets_of_few_tokens_are_recorded(cuda_device, T, E, S):
 def test_gelu_in_its_tails(cuda_device):
     """Zero weights and b1 alone: every block of 128 hidden values is one GELU value,
     which the second product (the identity) returns as 448 * scale.  b2 takes the
-    exact value away, so y is the error, in the units of the value: GELU 17 * 2^-24
-    (at most 32 by its terms), scale, product, sum and b2 one each: below 2^-18.
+    exact value away, so y is the error, in the units of the value: GELU 49 * 2^-24,
+    scale, product, sum and b2 one each: below 2^-18.
     One, two and more tokens give the same bits."""
     d = 2048
     first = None
@@ -453,3 +453,24 @@ def test_scales_forty_binary_orders_apart(cuda_device):
     wl = syn.Workload("block", T=2, d_model=400, E=2, d_ff=272, top_k=1)     # and the form for few tokens
     cfg = nat.config_from_workload(wl)
     check(cfg, [1, 1], w, grouped(cfg, None, [1, 1], w, sld, cuda_device, 6, False), far=True)
+
+
+@pytest.mark.parametrize("T", [2, 200])
+def test_gelu_rows_that_are_not_finite_stay_alone(cuda_device, T):
+    wl = syn.Workload("block", T=T, d_model=256, E=2, d_ff=256, top_k=1, act="gelu")
+    cfg = nat.config_from_workload(wl)
+    sld = nat.fp8_block_sld(cfg)
+    w = syn.generate_fp8_block_experts(wl, sld, cuda_device)
+    r = grouped(cfg, None, [T - 1, 1], w, sld, cuda_device, 1, True)
+    want = r["y"].clone()
+    for bad in ("nan", "inf"):
+        x8, xs = r["x8"].clone(), r["xs"].clone()
+        if bad == "nan":
+            x8[T - 2, 3] = 0x7F
+        else:
+            xs[T - 2, 0] = float("inf")
+        nat.moe_grouped_ffn_fp8_block(cfg, x8, xs, r["offsets"], r["gate"], r["ex"], w["b1"], w["b2"], None, None, r["y"],
+                                      r["ws"])
+        keep = torch.arange(T, device=cuda_device) != T - 2
+        assert torch.equal(r["y"][keep], want[keep])
+        assert torch.isnan(r["y"][T - 2]).all() if bad == "nan" else not torch.isfinite(r["y"][T - 2]).any()
