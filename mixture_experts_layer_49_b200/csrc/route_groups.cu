@@ -284,9 +284,13 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int t) {
     return my_id;
 }
 
-// 1 / (1 + exp(-l)) within three units of 2^-23; 0 below -88.72, where exp(-l)
-// passes the largest fp32 number.
-__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+// 1 / (1 + exp(-l)) within 7 * 2^-24 of its value (expf 4, the sum 1, the reciprocal
+// 2); 0 below -88.72, where exp(-l) passes the largest fp32 number.
+__device__ __forceinline__ float sigmoid(float l) {
+    float s;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + expf(-l)));
+    return s;
+}
 
 // Scores of the lane's experts (0 for absent ones) and the factor that makes
 // them shares of 1.  A row whose logits are all -inf has no scores: all 0.
@@ -362,11 +366,11 @@ __device__ __forceinline__ float one_logit(const RouteArgs &a, int t, int e) {
 }
 
 // Error bounds.  A sigmoid key: expf is off by 4 * 2^-24 of its value (2 ulp), which
-// moves s by s (1 - s) of that, at most 2^-24; the sum and the quotient round by
-// 2^-24 each: together at most 3 * 2^-24 (s <= 1); the sum with the bias by 2^-24 of
-// it.  A softmax key: the latter alone.  Two distances from the best key mx: besides
-// their keys, cut off at 2^-15 of them and one rounding (and 2^-140, what the cut
-// takes off a subnormal one).
+// moves s by s (1 - s) of that, at most 2^-24; the sum is off by 2^-24 and the
+// reciprocal by 2 * 2^-24: together at most 4 * 2^-24 (s <= 1); the sum with the bias
+// by 2^-24 of it.  A softmax key: the latter alone.  Two distances from the best key
+// mx: besides their keys, cut off at 2^-15 of them and one rounding (and 2^-140, what
+// the cut takes off a subnormal one).
 struct Bounds {
     float abs, rel;                                // of a key
     __device__ __forceinline__ explicit Bounds(const RouteArgs &a)

@@ -278,10 +278,10 @@ def test_gradient_of_an_id_that_stands_twice(cuda_device, equal, score, renorm):
 @pytest.mark.parametrize("lo,hi", [(-88.7, -87.0), (-88.7, -60.0), (-60.0, -50.0), (-30.0, -20.0), (-16.0, -8.0), (-8.0, 0.0),
                                    (0.0, 20.0), (-88.7, 3.0)])
 def test_sigmoid_scores_of_any_size(cuda_device, lo, hi):
-    """In units of 2^-24.  A score: expf 4 (2 ulp), sum and quotient 1 each, a
-    subnormal one (above 2^-128) 4 more: 10.  A gate: 10, the sum's 10 and 5
-    shuffles, quotient and factor: 27 < 32.  A score sum: 10, the sum's 10 and 13
-    additions, reciprocal and product, 32 tokens: 67 < 128."""
+    """In units of 2^-24.  A score: expf 4 (2 ulp), sum 1, reciprocal 2 (1 ulp), a
+    subnormal one (above 2^-128) 4 more: 11.  A gate: 11, the sum's 11 and 5
+    shuffles, quotient and factor: 29 < 32.  A score sum: 11, the sum's 11 and 13
+    additions, reciprocal and product, 32 tokens: 69 < 128."""
     g = torch.Generator(device=cuda_device).manual_seed(31)
     for E, groups in ((256, (8, 4, 2, 2.5)), (60, (5, 2, 1, 1.0))):
         logits = lo + (hi - lo) * torch.rand((64, E), generator=g, device=cuda_device)
