@@ -11,9 +11,9 @@
 // sums never leave fp32 and the partial products of 128 terms are the longest
 // chain that the tensor core rounds.
 //
-// Persistent CTAs of 384 threads, one to an SM, alone (128 rows x 256
-// accumulator columns, 4 stages of 48 KiB) or in pairs (256 x 256, 6 stages of
-// 32 KiB a CTA); SwiGLU's columns are 128 of the gate and 128 of the up product:
+// Persistent CTAs of 384 threads, one to an SM (128 rows x 256 accumulator
+// columns, 4 stages of 48 KiB); SwiGLU's columns are 128 of the gate and 128 of the
+// up product:
 //   warp 0       TMA producer
 //   warps 1, 2   TMEM allocator (1) and tcgen05.mma issuers of the even and odd
 //                K blocks
@@ -25,15 +25,22 @@
 // scales and no pass over H runs in between; the down projection adds the bias,
 // applies the gate and rounds once to bf16.
 //
-// Per K block and CTA the tensor core needs 512 cycles (128 x 256 x 128 products
-// at 8192 per cycle) and a pair's loop takes 835 (8192 x 28672 x 4096: 905 us
-// for the first runs, then the power limit holds the clock near 1.4 GHz and it
-// takes 1070).  The scaled sums make the difference: without the multiply-adds
-// the same loop runs at 600 cycles, without the TMEM loads too at 520, without
-// the copies still at 860.  None of these went below 825: half accumulators of
-// 128 columns with barriers of their own, loads of 32 columns beside the
-// multiply-adds of the last 32, packed f32x2 multiply-adds.  A library product of
-// these sizes with one scale per tensor, so without the sums, takes 757 us.
+// Per K block the tensor core needs 512 cycles (128 x 256 x 128 products at 8192
+// per cycle) and the loop takes about 850, beside the power limit, which holds the
+// clock near 1.4 GHz in long runs.  The scaled sums make the difference: in the
+// same loop of a CTA pair, at 835 cycles, leaving out the multiply-adds gave 600,
+// the TMEM loads too 520, the copies 860.  None of these went below 825: half
+// accumulators of 128 columns with barriers of their own, loads of 32 columns
+// beside the multiply-adds of the last 32, packed f32x2 multiply-adds.  A library
+// product of 8192 x 28672 x 4096 with one scale per tensor, so without the sums,
+// takes 757 us where a pair's took 905.
+//
+// CTA pairs (256-row tiles by cta_group::2, 32 KiB a CTA and K block instead of 48,
+// last blocks of 1..128 rows in a launch of their own) are not faster: one expert
+// of 8192 rows, 4096 x 14336, 1.55 ms either way, but 16384 tokens of the Qwen3
+// shape 945 us against 909, 4096 of the Mixtral shape 1725 against 1672, 8192
+// tokens with 128 experts of 7168 x 2048 4.03 ms against 3.74 (each at least three
+// runs in turn).
 //
 // Every mbarrier wait is bounded as in the other tensor-core kernels; a wait
 // that runs out records MOE_ERR_TIMEOUT, and the CTA lets its copies and
@@ -85,15 +92,13 @@ struct Params {
     int64_t ldo;
     float *out_scale;            // scale rows of the codes, ld_out_scale floats apart
     int64_t ld_out_scale;
-    int tail_mode;               // 1-CTA kernel: only last blocks of 1..128 rows
     uint64_t timeout_ns;
 };
 
-// Barriers and the tile table behind the stages; NS stages.
-template <int NS>
-struct TailT {
-    uint64_t full[NS];
-    uint64_t empty[NS];
+// Barriers and the tile table behind the stages.
+struct Tail {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
     uint64_t accf[2];
     uint64_t acce[2];
     uint64_t drain[2];
@@ -104,10 +109,8 @@ struct TailT {
     int mtiles[kMaxGroups];
     int rows[kMaxGroups];
     int row0[kMaxGroups];
-    int start[kMaxGroups];       // first row of the group that this launch computes
     float amax[2][2][BM];        // SwiGLU: the two halves' row maxima, two tiles deep
 };
-using Tail = TailT<STAGES>;
 // Output staging: 32 rows of 64 bytes per sums warp.
 constexpr uint32_t STG_BYTES = 32 * 64;
 constexpr size_t kStgOff = (STAGES * STAGE_BYTES + sizeof(Tail) + 1023) / 1024 * 1024;
@@ -125,11 +128,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t addr, uint32_t parity, uint64
     return __all_sync(0xffffffffu, mbar_wait(addr, parity, limit_ns));
 }
 
-template <class Tail>
 __device__ __forceinline__ bool aborted(const Tail &s) {
     return *reinterpret_cast<const volatile int *>(&s.abort_flag) != 0;
 }
-template <class Tail>
 __device__ __forceinline__ void fail(Tail &s, const Params &p, int where) {
     record_error(p.status, MOE_ERR_TIMEOUT, where);
     *reinterpret_cast<volatile int *>(&s.abort_flag) = 1;
@@ -137,7 +138,6 @@ __device__ __forceinline__ void fail(Tail &s, const Params &p, int where) {
 
 // The group of tile `tile`, from the group of an earlier one; mt runs fastest
 // within a group, so CTAs at work together share weight tiles through L2.
-template <class Tail>
 __device__ __forceinline__ void locate(const Tail &s, int tile, int &g, int &mt, int &nt) {
     while (s.tile_start[g + 1] <= tile) ++g;
     const int local = tile - s.tile_start[g], n = s.mtiles[g];
@@ -302,12 +302,9 @@ __device__ __forceinline__ bool finish_row(const Params &p, const RowCtx &c, flo
 }
 
 // The tile list of a launch from the device-side offsets: groups are the routed
-// experts and, last, the shared expert.  TILES_PAIR: 256-row blocks and a last
-// block of more than 128 rows; TILES_TAIL: a last block of 1..128 rows, the rest
-// of the same groups; TILES_ALL: 128-row blocks of everything.
-enum { TILES_ALL = 0, TILES_TAIL = 1, TILES_PAIR = 2 };
-template <int BNO, class Tail>
-__device__ __forceinline__ void build_tiles(Tail &s, const Params &p, int which) {
+// experts and, last, the shared expert.
+template <int BNO>
+__device__ __forceinline__ void build_tiles(Tail &s, const Params &p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.E + (p.has_shared ? 1 : 0);
     if (tid == 0) s.tile_start[0] = 0;
@@ -319,18 +316,10 @@ __device__ __forceinline__ void build_tiles(Tail &s, const Params &p, int which)
             record_error(p.status, MOE_ERR_DEVICE_BOUNDS, g);
             r0 = rows = 0;
         }
-        int start = 0, mt = (int)((rows + BM - 1) / BM);
-        const int rem = (int)(rows % (2 * BM));
-        if (which == TILES_TAIL) {
-            start = (int)rows - rem;
-            mt = (rem > 0 && rem <= BM) ? 1 : 0;
-        } else if (which == TILES_PAIR) {
-            mt = (int)(rows / (2 * BM)) + (rem > BM ? 1 : 0);
-        }
+        const int mt = (int)((rows + BM - 1) / BM);
         const int n = sh ? p.N_shared : p.N_routed;
         s.rows[g] = (int)rows;
         s.row0[g] = (int)r0;
-        s.start[g] = start;
         s.mtiles[g] = mt > 0 ? mt : 1;
         s.tile_start[g + 1] = mt * ((n + BNO - 1) / BNO);
     }
@@ -352,11 +341,9 @@ __device__ __forceinline__ void build_tiles(Tail &s, const Params &p, int which)
 }
 
 // The work of warps 4..11: two per TMEM lane quadrant, each half of the
-// columns.  PAIR: the CTA's rows are the rank-th 128 of a 256-row tile and the
-// accumulators are freed at the first CTA's barriers.
-template <int MODE, bool PAIR, class Tail>
-__device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tmem_base, uint32_t stg0, int total,
-                                           int tile0, int step, int rank) {
+// columns.
+template <int MODE>
+__device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tmem_base, uint32_t stg0, int total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q = warp & 3, half = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
@@ -365,16 +352,15 @@ __device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tm
     // columns of this warp: SwiGLU 64 gate and 64 up columns, else 128 in a row
     const uint32_t c0 = MODE == FB_SWIGLU ? half * 64 : half * 128;
     const uint32_t c1 = MODE == FB_SWIGLU ? 128 + half * 64 : half * 128 + 64;
-    constexpr int TM = PAIR ? 2 * BM : BM;
     uint32_t cnt = 0;
     uint32_t flip = 0;                                     // parity of the tiles this CTA has done
     bool ok = true;
     int g = 0;
-    for (int tile = tile0; tile < total && ok; tile += step, flip ^= 1u) {
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, flip ^= 1u) {
         int mt, nt;
         locate(s, tile, g, mt, nt);
         const bool sh = g >= p.E;
-        const int grow = s.start[g] + mt * TM + rank * BM + r_in_tile;
+        const int grow = mt * BM + r_in_tile;
         const int64_t first = sh ? 0 : (int64_t)s.row0[g];
         const int64_t a_off = sh ? p.shared_a_row : 0, o_off = sh ? p.shared_out_row : 0;
         const RowCtx c = row_ctx<MODE>(p, sh, g, nt, half, a_off + first + grow, a_off + first,
@@ -402,10 +388,7 @@ __device__ __forceinline__ void sums_warps(Tail &s, const Params &p, uint32_t tm
             tmem_ld32x2(ta + c1, ta + c1 + 32, v);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {                               // the accumulator is free: its words are in registers
-                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acce[ab]), 0));
-                else mbar_arrive(smem_u32(&s.acce[ab]));
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&s.acce[ab]));     // free: its words are in registers
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[64 + i] = fmaf(v[i], s1, acc[64 + i]);
         }
@@ -446,14 +429,8 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
-    // Last blocks (tail mode) touch only rows the CTA-pair launch before them
-    // leaves alone and read only what the kernel before that wrote (complete
-    // once the pair launch started, which is when this launch can begin), so
-    // they start at once on the SMs the pair launch frees and wait for it only
-    // before exiting: whatever waits for this launch then sees both results.
-    if (p.tail_mode) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    else pdl_wait_then_release();
-    build_tiles<BNO>(s, p, p.tail_mode ? TILES_TAIL : TILES_ALL);
+    pdl_wait_then_release();
+    build_tiles<BNO>(s, p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -476,7 +453,7 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 locate(s, tile, g, mt, nt);
                 const bool sh = g >= p.E;
                 const int nk = ((sh ? p.K_shared : p.K_routed) + BK - 1) / BK;
-                const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + s.start[g] + mt * BM;
+                const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + mt * BM;
                 const CUtensorMap *mA = sh ? &tmAs : &tmA;
                 const CUtensorMap *mB = sh ? &tmBs : &tmB;
                 const CUtensorMap *mB2 = sh ? &tmBs2 : &tmB2;
@@ -540,7 +517,7 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ================= scaled sums and epilogue: warps 4..11
-        sums_warps<MODE, false>(s, p, tmem_base, base + (uint32_t)kStgOff, total, blockIdx.x, gridDim.x, 0);
+        sums_warps<MODE>(s, p, tmem_base, base + (uint32_t)kStgOff, total);
     }
 
     tc_fence_before();
@@ -550,184 +527,19 @@ fp8_block_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
     }
-    if (p.tail_mode) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// ============================================================================
-// CTA pairs: a cluster of two computes 256 rows x 256 accumulator columns with
-// tcgen05.mma.cta_group::2.  Each CTA loads its own 128 A rows and half of the B
-// rows (SwiGLU: gate rows in the first CTA, up rows in the second), so a K block
-// moves 32 KiB per CTA through L2 instead of 48; at 48 KiB the L2 limits the
-// 1-CTA kernel to about 850 cycles a block.  The first CTA issues the products;
-// its full barriers collect both CTAs' copies, its commits reach both CTAs'
-// empty and accumulator-full barriers, and both CTAs' sums warps free the
-// accumulators at its barriers.
-constexpr int P_STAGES = 6;
-constexpr uint32_t P_STAGE_BYTES = A_BYTES + B_BYTES / 2;
-constexpr uint32_t kIdescPair = make_idesc_e4m3(2 * BM, BN);
-using PairTail = TailT<P_STAGES>;
-constexpr size_t kPairStgOff = (P_STAGES * P_STAGE_BYTES + sizeof(PairTail) + 1023) / 1024 * 1024;
-constexpr size_t kPairSmemBytes = 1024 + kPairStgOff + 8 * STG_BYTES;
-static_assert(kPairSmemBytes <= 227 * 1024, "pair kernel shared memory");
-
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-fp8_block_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
-                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
-                    const __grid_constant__ CUtensorMap tmBs, const __grid_constant__ CUtensorMap tmBs2,
-                    const __grid_constant__ Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_addr = smem_u32(smem_raw);
-    const uint32_t base = (raw_addr + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (base - raw_addr);
-    PairTail &s = *reinterpret_cast<PairTail *>(smem + P_STAGES * P_STAGE_BYTES);
-    const uint32_t smA = base;
-    const uint32_t smB = base + P_STAGES * A_BYTES;
-
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const uint32_t rank = cluster_ctarank();
-    const int pair = (int)cluster_id_x(), npairs = (int)ncluster_x();
-    constexpr int BNO = MODE == FB_SWIGLU ? 128 : 256;
-
-    if (tid == 0) {
-        s.abort_flag = 0;
-        for (int i = 0; i < P_STAGES; ++i) { mbar_init(smem_u32(&s.full[i]), 1); mbar_init(smem_u32(&s.empty[i]), 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&s.accf[i]), 1); mbar_init(smem_u32(&s.acce[i]), 16); }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.xch[i]), 2);
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    if (warp == 1) tmem_alloc_pair(smem_u32(&s.tmem_base), TMEM_COLS);   // warp 1 of both CTAs
-    if (tid == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB2) : "memory");
-    }
-    pdl_wait_then_release();
-    build_tiles<BNO>(s, p, TILES_PAIR);
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();                                        // both CTAs' barriers are initialised
-    tc_fence_after();
-    const int total = s.tile_start[p.E + (p.has_shared ? 1 : 0)];
-    const uint32_t tmem_base = s.tmem_base;
-
-    // registers as in the 1-CTA kernel
-    if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-      if (warp == 0) {
-        // ================= TMA producer (both CTAs)
-        if (lane == 0) {
-            uint32_t i = 0;                                // K blocks loaded
-            int g = 0;
-            bool ok = true;
-            for (int tile = pair; tile < total && ok && !aborted(s); tile += npairs) {
-                int mt, nt;
-                locate(s, tile, g, mt, nt);
-                const bool sh = g >= p.E;
-                const int nk = ((sh ? p.K_shared : p.K_routed) + BK - 1) / BK;
-                const int a_row = (sh ? (int)p.shared_a_row : s.row0[g]) + mt * 2 * BM + (int)rank * BM;
-                const CUtensorMap *mA = sh ? &tmAs : &tmA;
-                const CUtensorMap *mB = (MODE == FB_SWIGLU && rank == 1) ? (sh ? &tmBs2 : &tmB2) : (sh ? &tmBs : &tmB);
-                const int b_row = MODE == FB_SWIGLU ? nt * 128 : nt * BN + (int)rank * 128;
-                const int e = sh ? 0 : g;
-                for (int kb = 0; kb < nk; ++kb, ++i) {
-                    const uint32_t stage = i % P_STAGES, phase = (i / P_STAGES) & 1u;
-                    if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, p.timeout_ns)) { fail(s, p, 71); ok = false; break; }
-                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[stage]), 2 * P_STAGE_BYTES);
-                    tma_load_2d_pair(smA + stage * A_BYTES, mA, fb, kb * BK, a_row);
-                    tma_load_3d_pair(smB + stage * (B_BYTES / 2), mB, fb, kb * BK, b_row, e);
-                }
-            }
-            // every copy has landed before the pair may end: the last use of each stage
-            if (rank == 0)
-                for (uint32_t j = i > P_STAGES ? i - P_STAGES : 0; j < i; ++j)
-                    if (!mbar_wait(smem_u32(&s.full[j % P_STAGES]), (j / P_STAGES) & 1u, p.timeout_ns)) fail(s, p, 75);
-        }
-      } else if (warp < 3) {
-        // ================= MMA issuers (first CTA): even and odd K blocks
-        if (rank == 0) {
-            const uint32_t ab = warp - 1;
-            const bool leader = elect_lane();
-            const uint64_t da0 = sdesc(smA), db0 = sdesc(smB);
-            const uint32_t dtm = tmem_base + ab * BN;
-            uint32_t cnt = 0;
-            bool ok = true;
-            for (int tile = pair; tile < total && ok && !aborted(s); tile += npairs) {
-                const uint32_t nk = ((tile >= s.tile_start[p.E] ? p.K_shared : p.K_routed) + BK - 1) / BK;
-                uint32_t i = cnt + ((cnt ^ ab) & 1u);
-                cnt += nk;
-                for (; i < cnt; i += 2) {
-                    const uint32_t stage = i % P_STAGES, phase = (i / P_STAGES) & 1u, aphase = (i >> 1) & 1u;
-                    if (!warp_wait(smem_u32(&s.acce[ab]), aphase ^ 1u, p.timeout_ns)) { if (leader) fail(s, p, 72); ok = false; break; }
-                    if (!warp_wait(smem_u32(&s.full[stage]), phase, p.timeout_ns)) { if (leader) fail(s, p, 73); ok = false; break; }
-                    tc_fence_after();
-                    const uint64_t da = da0 + stage * (A_BYTES >> 4), db = db0 + stage * (B_BYTES >> 5);
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < BK / 32; ++k) mma_e4m3_pair(dtm, da + k * 2, db + k * 2, kIdescPair, k ? 1u : 0u);
-                        mma_commit_pair(smem_u32(&s.accf[ab]), (uint16_t)0x3);
-                        mma_commit_pair(smem_u32(&s.empty[stage]), (uint16_t)0x3);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (aborted(s) && leader) {                    // products in flight end before TMEM is freed
-                mma_commit_pair(smem_u32(&s.drain[ab]), (uint16_t)0x1);
-                if (!mbar_wait(smem_u32(&s.drain[ab]), 0, p.timeout_ns)) fail(s, p, 76);
-            }
-            __syncwarp();
-        }
-      }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        sums_warps<MODE, true>(s, p, tmem_base, base + (uint32_t)kPairStgOff, total, pair, npairs, (int)rank);
-    }
-
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();                                        // no CTA leaves while its peer may still signal it
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc_pair(tmem_base, TMEM_COLS);
-    }
-}
-
-// CTAs of a launch of `kernel` on the current device, found once per device
-// (0: not yet); pair: as many clusters of two as fit at a time.
+// Lets `kernel` use its shared memory, once per device.
 template <typename K>
-cudaError_t grid_of(std::atomic<int> (&cache)[64], K kernel, size_t smem, int num_sms, bool pair, int *grid) {
+cudaError_t allow_smem(std::atomic<bool> (&done)[64], K kernel) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    *grid = cache[dev].load(std::memory_order_relaxed);
-    if (*grid) return cudaSuccess;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    int n = num_sms;
-    if (pair) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
-        cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
-        n *= 2;
-    }
-    cache[dev].store(n, std::memory_order_relaxed);
-    *grid = n;
-    return cudaSuccess;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 // Tensor maps of one product: A and weights.
@@ -735,23 +547,12 @@ struct Maps {
     CUtensorMap A, As, B, B2, Bs, Bs2;
 };
 
-// One product.  few: one launch of 128-row tiles; else the pair launch and,
-// overlapping it, the last blocks of 1..128 rows.
 template <int MODE>
-cudaError_t launch_product(const Maps &m, Params p, bool few, int num_sms, cudaStream_t st, bool pdl) {
-    static std::atomic<int> one[64], two[64];
-    int grid = 0;
-    cudaError_t e;
-    p.tail_mode = few ? 0 : 1;
-    if (!few) {
-        if ((e = grid_of(two, fp8_block_gemm_pair<MODE>, kPairSmemBytes, num_sms, true, &grid)) != cudaSuccess) return e;
-        e = launch_kernel(fp8_block_gemm_pair<MODE>, dim3(grid), dim3(kThreads), kPairSmemBytes, st, pdl, m.A, m.As, m.B,
-                          m.B2, m.Bs, m.Bs2, p);
-        if (e != cudaSuccess) return e;
-        pdl = true;
-    }
-    if ((e = grid_of(one, fp8_block_gemm<MODE>, kSmemBytes, num_sms, false, &grid)) != cudaSuccess) return e;
-    return launch_kernel(fp8_block_gemm<MODE>, dim3(grid), dim3(kThreads), kSmemBytes, st, pdl, m.A, m.As, m.B, m.B2, m.Bs,
+cudaError_t launch_product(const Maps &m, const Params &p, int num_sms, cudaStream_t st, bool pdl) {
+    static std::atomic<bool> done[64];
+    const cudaError_t e = allow_smem(done, fp8_block_gemm<MODE>);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(fp8_block_gemm<MODE>, dim3(num_sms), dim3(kThreads), kSmemBytes, st, pdl, m.A, m.As, m.B, m.B2, m.Bs,
                          m.Bs2, p);
 }
 
@@ -765,7 +566,7 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     const uint64_t routed = a.routed_rows > 0 ? (uint64_t)a.routed_rows : 1;
     const uint64_t all = (uint64_t)(a.shared_base + (has_sh ? a.T : 0));
     const uint64_t d = a.d, F = a.F, S = a.S;
-    // weight boxes of 128 rows: half a tile, or a pair CTA's share of one
+    // weight boxes of 128 rows: half a tile
     auto weights = [](CUtensorMap *m, const uint8_t *w, uint64_t in, uint64_t out, uint64_t n) {
         return make_map(m, 3, w, in, out, n, in, out * in, 128, 1);
     };
@@ -798,19 +599,8 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     p.out = a.H8; p.ldo = a.hF;
     p.out_scale = a.h_scale; p.ld_out_scale = a.ld_hs / 4;
     p.timeout_ns = 2000000000ull;
-    // Pairs where the tiles fill the SMs many times over (Mixtral shape, 4096
-    // tokens: 1552 us against 1709 for single CTAs, which move half as much again
-    // through L2 and draw more power); else single CTAs, twice as many tiles and
-    // one launch (2000 rows of 16 ragged experts 69 us against 84).
-    auto few_tiles = [&](int64_t n_routed, int64_t n_shared, int64_t bno) {
-        const int64_t blocks = a.routed_rows / BM + (a.routed_rows < a.E ? a.routed_rows : a.E) / 2;
-        const int64_t tiles = blocks * ((n_routed + bno - 1) / bno) +
-                              (has_sh ? (a.T + BM - 1) / BM * ((n_shared + bno - 1) / bno) : 0);
-        return tiles < 8 * (int64_t)a.num_sms;
-    };
-    bool few = few_tiles(a.F, a.S, swiglu ? 128 : BN);
-    cudaError_t e = swiglu ? launch_product<FB_SWIGLU>(m1, p, few, a.num_sms, st, a.pdl)
-                           : launch_product<FB_GELU>(m1, p, few, a.num_sms, st, a.pdl);
+    cudaError_t e = swiglu ? launch_product<FB_SWIGLU>(m1, p, a.num_sms, st, a.pdl)
+                           : launch_product<FB_GELU>(m1, p, a.num_sms, st, a.pdl);
     if (e != cudaSuccess) return e;
 
     p.K_routed = a.F; p.K_shared = a.S; p.N_routed = a.d; p.N_shared = a.d;
@@ -821,8 +611,7 @@ cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st) {
     p.row_gate = a.row_gate;
     p.out = a.y_perm; p.ldo = a.d;
     p.out_scale = nullptr; p.ld_out_scale = 0;
-    few = few_tiles(a.d, a.d, BN);
-    return launch_product<FB_DOWN>(m2, p, few, a.num_sms, st, true);
+    return launch_product<FB_DOWN>(m2, p, a.num_sms, st, true);
 }
 
 }  // namespace moe

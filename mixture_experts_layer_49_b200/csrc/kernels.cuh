@@ -374,9 +374,11 @@ struct FfnFp8BlockArgs {
 };
 cudaError_t launch_ffn_fp8_block(const FfnFp8BlockArgs &a, cudaStream_t st);
 // The form for one or two tokens (fp8_block_decode.cu).  Measured against the tile
-// kernels, us: Qwen3 shape T 1 14.6 / 26.3, T 2 25.3 / 32.2, T 8 69.7 / 63.1; 32
-// experts of 7168 x 2048 and a shared one T 1 86 / 89, T 4 245 / 198; Mixtral shape
-// T 1 84 / 139, T 4 248 / 238.
+// kernels with other experts in every call, us: Qwen3 shape T 1 15.1 / 26.9, T 2
+// 24.0 / 30.4, T 3 32.1 / 36.3, T 4 43.1 / 45.2; Mixtral shape T 1 81 / 110, T 2 150 /
+// 171, T 3 223 / 198; 32 experts of 7168 x 2048 and a shared one T 1 85 / 88, T 2 146 /
+// 136, T 3 204 / 157.  (What decides is the rows and experts that are hit: with one
+// expert a token the Qwen3 shape takes 9.4 / 25.3 for T 3.)
 constexpr int kFp8BlockDecodeT = 2;
 cudaError_t launch_ffn_fp8_block_decode(const FfnFp8BlockArgs &a, cudaStream_t st);
 

@@ -134,7 +134,7 @@ def test_grouped_ffn(cuda_device, T, d, E, F, k, act, S, counts):
     check(cfg, counts, w, r)
 
 
-# enough tiles for CTA pairs in one of the products, with last blocks of 1, 127, 128, 129
+# thousands of tiles in one of the products, with last blocks of 1, 127, 128, 129
 # and more rows, experts without rows, the shared expert and biases
 @pytest.mark.parametrize("T,d,E,F,k,act,S,counts", [
     (4600, 144, 5, 2064, 2, "swiglu", 272, [4000, 129, 0, 4815, 256]),
@@ -338,8 +338,8 @@ def test_group_limited_training(cuda_device):
         assert (b - 2 * a).norm() <= 2.0 ** -16 * b.norm() + 1e-30, n
 
 
-# T, d, E, F, k, S: one CTA a tile, CTA pairs in the first product, in both with the
-# shared expert, and the form for one and two tokens
+# T, d, E, F, k, S: few tiles and many, in either product, with and without the shared
+# expert, and the form for one and two tokens
 @pytest.mark.parametrize("T,d,E,F,k,act,S", [
     (2000, 1040, 16, 400, 2, "swiglu", 0), (9000, 144, 8, 2064, 2, "swiglu", 272), (15000, 1040, 5, 272, 2, "swiglu", 144),
     (2000, 1040, 16, 400, 1, "gelu", 0), (2, 2048, 64, 768, 8, "swiglu", 768),
