@@ -566,16 +566,19 @@ MOE_API moe_status moe_grouped_ffn_fp8_block(const moe_config *cfg, const uint8_
 
 /* ---- Group-limited routing -------------------------------------------------
  * The E experts form n_group equal groups of consecutive ids (the experts of
- * one node), and a token only uses experts of its topk_group best groups,
- * which bounds the ranks its row travels to ("Fine-Tuning Mixture of Experts
- * (MoE) Models: Router Optimization Techniques", Why It Matters 2: dispatch
- * traffic).  With the scores and selection keys of moe_router_topk:
+ * one node), and a token only uses experts of its topk_group best groups, as
+ * models are trained whose rows may travel to a few ranks only ("Fine-Tuning
+ * Mixture of Experts (MoE) Models: Router Optimization Techniques", Why It
+ * Matters 2: dispatch traffic; the moe_ep_* calls themselves take rows as
+ * routed, by whichever call).  With the scores and selection keys of moe_router_topk:
  *   group score = the sum of the group's group_top (1 or 2) largest keys;
  *   the topk_group groups of the largest score stay, the top_k largest keys
  *   inside them are chosen, best first; equal keys and equal groups go to the
  *   lower id; gates as in moe_router_topk, times gate_scale.
- * Keys are compared by their 64-bit values.  A logit of -inf is an expert that
- * is chosen last; a row whose chosen scores sum to 0 gets gates of 0; NaN keys
+ * Keys are compared by their 64-bit values.  A softmax logit of -inf is an expert
+ * that is chosen last; a sigmoid one has score 0, so its key is its bias.  fp32
+ * sigmoids are 0 below a logit of -88.72.  A row whose chosen scores sum to 0 gets
+ * gates of 0, and no gradient through them; NaN keys
  * rank below all others.  n_group divides E, group_top <= E / n_group, top_k <=
  * topk_group * E / n_group, gate_scale > 0 (else MOE_ERR_INVALID_ARG).
  * n_group = 1 is the unrestricted choice.  The struct is a host object read

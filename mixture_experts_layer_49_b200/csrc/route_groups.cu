@@ -24,13 +24,16 @@
 // largest, then its id, so one redux.sync.min finds the best candidate with the
 // lowest id, and a lane's candidates sort with plain minima and maxima.
 //
-// The floor is the logits read once (2.8 us for 16384 x 256); the selection's
-// instructions bound it (8 groups of which 4 are kept, k = 8), at a register limit
-// that keeps 32 warps on an SM: 22.9 us there, 12.4 us
-// for 16384 x 128 softmax without groups, 5.5 us for 16 tokens of 256.  With 85
-// registers and 24 warps the same took 22.5, 13.9 and 5.3 us.  Rounds over 64-bit keys
-// took 50 us; the doubtful tokens in a pass of their own after the others 23 (14.4
-// against 7.5 for 1000 tokens).
+// The floor is the logits read once (2.8 us for 16384 x 256).  What bounds it is
+// the latency of a token's serial rounds (8 groups of which 4 are kept, k = 8), with
+// 60 % of the issue slots used, at a register limit that keeps 32 warps on an SM:
+// 22.0 us there, 13.0 us for 16384 x 128 softmax without groups, 5.6 us for 16 tokens
+// of 256.  Rows whose keys all tie, or that choose keys of -inf, repeat the selection
+// in 64 bits: 76 us for 16384 x 256 equal sigmoids, 44 for 16384 x 128 equal logits.
+// With 85 registers and 24 warps the fp32 path took 22.5 instead of 20.6, 13.9 instead
+// of 12.4 and 5.3 instead of 5.5.  Rounds over 64-bit keys took 50 us; the doubtful
+// tokens in a pass of their own after the others 23 (14.4 against 7.5 for 1000
+// tokens).
 #include "common.cuh"
 #include "kernels.cuh"
 
