@@ -181,8 +181,8 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const F (&k
         uint32_t lo = ordered((float)wk), hi = ordered((float)bd);
         lo = __reduce_min_sync(kAll, lo);
         hi = __reduce_max_sync(kAll, hi);
-        // -inf may be a sum that passed the fp32 range: 64 bits tell
-        *close = lo < hi || lo == ordered(-INFINITY);
+        // an infinite one may be a sum that passed the fp32 range: 64 bits tell
+        *close = lo < hi || lo == ordered(-INFINITY) || hi == ordered(INFINITY);
     }
     return mask;
 }

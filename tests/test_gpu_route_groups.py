@@ -362,3 +362,16 @@ def test_masks_of_the_lowest_value_beside_infinite_ones(cuda_device, E, size):
             idx, _, _ = run(l, None, k, (n, topk_group, group_top, 1.0), "softmax")
             want = ref.select(l.cpu(), None, k, n, topk_group, group_top, "softmax")
             assert torch.equal(idx.cpu(), want), (topk_group, group_top, k)
+
+
+@pytest.mark.parametrize("E,n", [(32, 8), (250, 10), (60, 5), (256, 8)])
+def test_group_scores_past_the_fp32_range(cuda_device, E, n):
+    """Keys of 1e38 and more: sums of two pass the fp32 range on either side."""
+    g = torch.Generator().manual_seed(51)
+    up = 1e38 + 2.4e38 * torch.rand((8, E), generator=g)
+    l = torch.cat([up, -up, torch.where(torch.rand((8, E), generator=g) < 0.5, up, -up)]).to(cuda_device)
+    bias = 300.0 * torch.randn(E, generator=g)
+    for topk_group in (1, n // 2, n - 1):
+        for b in (None, bias):
+            idx, _, _ = run(l, None if b is None else b.to(cuda_device), 4, (n, topk_group, 2, 1.0), "softmax")
+            assert torch.equal(idx.cpu(), ref.select(l.cpu(), b, 4, n, topk_group, 2, "softmax")), topk_group
