@@ -576,9 +576,10 @@ MOE_API moe_status moe_grouped_ffn_fp8_block(const moe_config *cfg, const uint8_
  *   inside them are chosen, best first; equal keys and equal groups go to the
  *   lower id; gates as in moe_router_topk, times gate_scale.
  * Keys are compared by their 64-bit values.  A softmax logit of -inf is an expert
- * that is chosen last; a sigmoid one has score 0, so its key is its bias.  fp32
- * sigmoids are 0 below a logit of -88.72.  A row whose chosen scores sum to 0 gets
- * gates of 0, and no gradient through them; NaN keys
+ * that is chosen last; a sigmoid one has score 0, so its key is its bias.  Scores
+ * are fp32: a sigmoid is 0 below a logit of -88.72, a softmax score 104 below the
+ * row's largest logit.  A row whose chosen scores sum to 0 gets gates of 0, and no
+ * gradient through them; NaN keys
  * rank below all others.  n_group divides E, group_top <= E / n_group, top_k <=
  * topk_group * E / n_group, gate_scale > 0 (else MOE_ERR_INVALID_ARG).
  * n_group = 1 is the unrestricted choice.  The struct is a host object read
